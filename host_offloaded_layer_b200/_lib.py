@@ -78,6 +78,10 @@ class mt_adamw_cfg(ctypes.Structure):
                 ("n_threads", c_i32)]
 
 
+class mt_muon_cfg(ctypes.Structure):
+    _fields_ = [("momentum", c_f32), ("nesterov", c_i32), ("steps", c_i32), ("eps", c_f32), ("scale", c_f32)]
+
+
 mt_grad_sink = ctypes.CFUNCTYPE(c_i32, c_i32, ctypes.POINTER(c_f32), c_u64, c_vp)
 mt_head_hook = ctypes.CFUNCTYPE(c_i32, c_vp, c_vp, c_vp, c_vp)
 
@@ -100,6 +104,12 @@ _SIGS = {
     "mt_rmsnorm_bwd_workspace_bytes": (c_u64, [c_i64, c_i32]),
     "mt_rmsnorm_bwd": (c_i32, [_P, _P, _P, _P, _P, _P, _P, c_i64, c_i32, _P, c_u64, _P]),
     "mt_rmsnorm_bwd_noalloc": (c_i32, [_P, _P, _P, _P, _P, _P, _P, c_i64, c_i32, _P]),
+    "mt_layernorm_fwd": (c_i32, [_P, c_i64, _P, _P, _P, c_i64, _P, _P, c_i64, c_i32, c_f32, _P]),
+    "mt_layernorm_bwd_workspace_bytes": (c_u64, [c_i64, c_i32]),
+    "mt_layernorm_bwd": (c_i32, [_P, c_i64, _P, c_i64, _P, _P, _P, _P, c_i64, _P, c_i64, _P, _P, c_i64, c_i32, _P,
+                                 c_u64, _P]),
+    "mt_mrope": (c_i32, [_P, c_i64, _P, c_i64, _P, c_i64, ctypes.POINTER(c_i32), c_i32, c_i64, c_i32, c_i32, c_f32, c_i32,
+                         c_i32, c_i32, _P]),
     "mt_rope": (c_i32, [_P, c_i64, c_i32, c_i32, c_i32, c_i32, c_f32, c_i32, _P]),
     "mt_swiglu_fwd": (c_i32, [_P, _P, c_i64, c_i32, _P]),
     "mt_swiglu_bwd": (c_i32, [_P, _P, _P, c_i64, c_i32, _P]),
@@ -135,6 +145,9 @@ _SIGS = {
     "mt_host_optimizer_create": (c_i32, [c_vp, ctypes.POINTER(mt_adamw_cfg), ctypes.POINTER(c_vp)]),
     "mt_host_optimizer_sink": (c_i32, [c_i32, ctypes.POINTER(c_f32), c_u64, c_vp]),
     "mt_host_optimizer_destroy": (None, [c_vp]),
+    "mt_muon_workspace_bytes": (c_u64, [c_i64, c_i64]),
+    "mt_muon_update": (c_i32, [_P, c_i64, _P, _P, c_i64, _P, c_i64, c_i64, c_i64, ctypes.POINTER(mt_muon_cfg), _P, c_u64,
+                               _P]),
     "mt_schedule_len": (c_i32, [c_i32, c_i32]),
     "mt_schedule": (c_i32, [c_i32, c_i32, c_i32, ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
                             ctypes.POINTER(c_i32), ctypes.POINTER(c_i32)]),
@@ -257,6 +270,30 @@ def mt_rmsnorm_bwd(dy, x, g, rstd, dres, dx, dg, rows, H, ws, ws_bytes, stream=N
 def mt_rmsnorm_bwd_noalloc(dy, x, g, rstd, dres, dx, dg, rows, H, stream=None):
     _check(load().mt_rmsnorm_bwd_noalloc(_ptr(dy), _ptr(x), _ptr(g), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dg), rows,
                                          H, _stream(stream)))
+
+
+def mt_layernorm_fwd(x, ld_x, g, b, y, ld_y, mean, rstd, rows, H, eps, stream=None):
+    _check(load().mt_layernorm_fwd(_ptr(x), ld_x, _ptr(g), _ptr(b), _ptr(y), ld_y, _ptr(mean), _ptr(rstd), rows, H, eps,
+                                   _stream(stream)))
+
+
+def mt_layernorm_bwd_workspace_bytes(rows, H) -> int:
+    return load().mt_layernorm_bwd_workspace_bytes(rows, H)
+
+
+def mt_layernorm_bwd(dy, ld_dy, x, ld_x, g, mean, rstd, dres, ld_dres, dx, ld_dx, dg, db, rows, H, ws, ws_bytes,
+                     stream=None):
+    _check(load().mt_layernorm_bwd(_ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(g), _ptr(mean), _ptr(rstd), _ptr(dres), ld_dres,
+                                   _ptr(dx), ld_dx, _ptr(dg), _ptr(db), rows, H, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def mt_mrope(x, ld_x, y, ld_y, pos, ld_pos, sections, rows, n_heads, head_dim, theta, interleaved=False, per_axis=False,
+             inverse=False, stream=None):
+    """sections: the pairs of each axis (a sequence of ints; its length is the number of axes)."""
+    n = len(sections)
+    _check(load().mt_mrope(_ptr(x), ld_x, _ptr(y), ld_y, _ptr(pos), ld_pos, (c_i32 * n)(*sections), n, rows, n_heads,
+                           head_dim, theta, 1 if interleaved else 0, 1 if per_axis else 0, 1 if inverse else 0,
+                           _stream(stream)))
 
 
 def mt_rope(x, ld, B, T, n_heads, head_dim, theta, inverse, stream=None):
@@ -421,6 +458,19 @@ def mt_host_optimizer_sink(layer, grad, n, opt):
 def optimizer_sink():
     """The library's AdamW sink as a callable for mt_stream_step (pass the optimizer as `user`)."""
     return ctypes.cast(load().mt_host_optimizer_sink, mt_grad_sink)
+
+
+def make_muon_cfg(momentum=0.95, nesterov=True, steps=5, eps=1e-7, scale=1.0) -> mt_muon_cfg:
+    return mt_muon_cfg(momentum, 1 if nesterov else 0, steps, eps, scale)
+
+
+def mt_muon_workspace_bytes(rows, cols) -> int:
+    return load().mt_muon_workspace_bytes(rows, cols)
+
+
+def mt_muon_update(g, ld_g, m_in, m_out, ld_m, o, ld_o, rows, cols, cfg, ws, ws_bytes, stream=None):
+    _check(load().mt_muon_update(_ptr(g), ld_g, _ptr(m_in), _ptr(m_out), ld_m, _ptr(o), ld_o, rows, cols,
+                                 ctypes.byref(cfg), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def mt_embed_fwd(tokens, E, x, M, H, V, bad_tokens, stream=None):

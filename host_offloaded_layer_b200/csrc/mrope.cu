@@ -1,0 +1,171 @@
+// Rotary positions with several axes (time, height, width of image and video tokens): rotate-half RoPE in
+// which every rotated pair of a head takes its position from one of the axes.
+//
+//   R = 2 * sum(sections) columns of each head rotate, pair i = (i, i + R/2) by angle pos[axis(i)][row] * omega_i:
+//   (a, b) -> (a cos - b sin, b cos + a sin); the columns behind R are copied.
+//
+// Bound by HBM: 4 bytes an element, against 3 flops. What could cost more than that is the angles, and they
+// are one per token and pair, shared by all heads: a CTA forms the (cos, sin) of a tile of tokens in shared
+// memory first and then rotates the tile's heads from it. omega is taken in turns (omega / 2 pi) in fp64 on
+// the host; position * turns is rounded to its fraction of a turn in fp64, so that a position of 2^31 keeps
+// an angle error below 5e-7, and only the fraction goes through the fp32 sincospi: two fp64 operations an
+// angle instead of an fp64 sincos.
+#include <algorithm>
+#include <cmath>
+
+#include "mt_internal.h"
+#include "vec.cuh"
+
+namespace mt {
+namespace {
+
+using namespace vec;
+
+constexpr int MAX_PAIRS = 128, MAX_AXES = 8;
+constexpr int THREADS = 256;
+constexpr int TABLE = 2048;  // (cos, sin) pairs of a tile: 16 KiB
+
+struct Mrope {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* y;
+  const int32_t* pos;
+  int64_t ld_x, ld_y, ld_pos, rows;
+  int heads, d, pairs, tile;  // tile: tokens of a tile, tile * pairs <= TABLE
+  float sign;
+  uint8_t axis[MAX_PAIRS];
+  double turns[MAX_PAIRS];
+};
+
+template <int VEC>
+__global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ Mrope a) {
+  using V = typename Raw<VEC>::type;
+  __shared__ float2 table[TABLE];
+  const int rot = a.pairs / VEC;                                       // rotated vectors of a head half
+  const int tail = a.x == a.y ? 0 : (a.d - 2 * a.pairs) / VEC;         // vectors to copy behind them
+  const int per_head = rot + tail, per_token = per_head * a.heads;
+  const int64_t tiles = (a.rows + a.tile - 1) / a.tile;
+  for (int64_t tl = blockIdx.x; tl < tiles; tl += gridDim.x) {
+    const int64_t row0 = tl * a.tile;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tile), a.rows - row0));
+    __syncthreads();  // the last tile's table is read
+    for (int e = threadIdx.x; e < tokens * a.pairs; e += THREADS) {
+      const int tok = e / a.pairs, i = e - tok * a.pairs;
+      const double p = static_cast<double>(a.pos[a.axis[i] * a.ld_pos + row0 + tok]) * a.turns[i];
+      float s, c;
+      sincospif(2.0f * static_cast<float>(p - rint(p)), &s, &c);
+      table[e] = make_float2(c, a.sign * s);
+    }
+    __syncthreads();
+    const int64_t items = static_cast<int64_t>(tokens) * per_token;
+    for (int64_t it = threadIdx.x; it < items; it += THREADS) {
+      const int tok = static_cast<int>(it / per_token), in_token = static_cast<int>(it - static_cast<int64_t>(tok) * per_token);
+      const int head = in_token / per_head, v = in_token - head * per_head;
+      const int64_t at = static_cast<int64_t>(head) * a.d;
+      const __nv_bfloat16* xh = a.x + (row0 + tok) * a.ld_x + at;
+      __nv_bfloat16* yh = a.y + (row0 + tok) * a.ld_y + at;
+      if (v < rot) {
+        const V lo = *reinterpret_cast<const V*>(xh + v * VEC), hi = *reinterpret_cast<const V*>(xh + a.pairs + v * VEC);
+        float l[VEC], h[VEC];
+        unpack(lo, l);
+        unpack(hi, h);
+        const float2* cs = table + tok * a.pairs + v * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float2 w = cs[i];
+          const float p = l[i], q = h[i];
+          l[i] = p * w.x - q * w.y;
+          h[i] = q * w.x + p * w.y;
+        }
+        V ol, oh;
+        pack(ol, l);
+        pack(oh, h);
+        *reinterpret_cast<V*>(yh + v * VEC) = ol;
+        *reinterpret_cast<V*>(yh + a.pairs + v * VEC) = oh;
+      } else {
+        const int c = 2 * a.pairs + (v - rot) * VEC;
+        *reinterpret_cast<V*>(yh + c) = *reinterpret_cast<const V*>(xh + c);
+      }
+    }
+  }
+}
+
+template <int VEC>
+mt_status go(Mrope a, cudaStream_t st) {
+  const int64_t per_token = static_cast<int64_t>(a.heads) * ((a.x == a.y ? 0 : a.d - 2 * a.pairs) + a.pairs) / VEC;
+  // tokens of a tile: at least a thread's worth of vectors, no more than the table holds, and no more than
+  // leaves every SM a few tiles
+  const int64_t sms = num_sms();
+  int64_t tile = std::max<int64_t>((THREADS + per_token - 1) / per_token, a.rows / (sms * 8));
+  tile = std::max<int64_t>(1, std::min<int64_t>(tile, TABLE / a.pairs));
+  a.tile = static_cast<int>(tile);
+  const int64_t tiles = (a.rows + tile - 1) / tile;
+  mrope_kernel<VEC><<<static_cast<unsigned>(std::min<int64_t>(tiles, sms * 8)), THREADS, 0, st>>>(a);
+  return launch_check("mrope_kernel");
+}
+
+}  // namespace
+}  // namespace mt
+
+using namespace mt;
+
+extern "C" mt_status mt_mrope(const mt_bf16* x, int64_t ld_x, mt_bf16* y, int64_t ld_y, const int32_t* pos, int64_t ld_pos,
+                              const int32_t* sections, int32_t n_axes, int64_t rows, int32_t n_heads, int32_t head_dim,
+                              float theta, int32_t interleaved, int32_t per_axis, int32_t inverse, void* stream) {
+  if (!sections || (rows != 0 && n_heads != 0 && (!x || !y || !pos))) return fail(MT_ERR_INVALID_ARG, "mrope: NULL pointer");
+  if (rows < 0 || n_heads < 0 || head_dim <= 0 || !(theta > 0.f) || !std::isfinite(theta))
+    return fail(MT_ERR_INVALID_ARG, "mrope: bad sizes or theta");
+  if (n_axes < 1 || n_axes > MAX_AXES) return fail(MT_ERR_INVALID_ARG, "mrope: 1 to %d axes, got %d", MAX_AXES, n_axes);
+  int64_t pairs = 0;
+  for (int i = 0; i < n_axes; ++i) {
+    if (sections[i] < 0) return fail(MT_ERR_INVALID_ARG, "mrope: section %d is negative", i);
+    pairs += sections[i];
+  }
+  if (pairs < 1 || 2 * pairs > head_dim)
+    return fail(MT_ERR_INVALID_ARG, "mrope: the sections hold %lld pairs, need 1 to head_dim / 2 = %d", (long long)pairs,
+                head_dim / 2);
+  if (pairs > MAX_PAIRS) return fail(MT_ERR_UNSUPPORTED, "mrope: at most %d rotated pairs a head", MAX_PAIRS);
+  const int64_t width = static_cast<int64_t>(n_heads) * head_dim;
+  if (width >= (1ll << 31)) return fail(MT_ERR_UNSUPPORTED, "mrope: heads of 2^31 columns and more");
+  if (ld_x < width || ld_y < width || ld_pos < rows) return fail(MT_ERR_INVALID_ARG, "mrope: ld too small");
+  if (x && x == y && ld_x != ld_y) return fail(MT_ERR_INVALID_ARG, "mrope: in place needs ld_x == ld_y");
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y);
+  if ((bits & 1) || (reinterpret_cast<uintptr_t>(pos) & 3))
+    return fail(MT_ERR_ALIGNMENT, "mrope: pointers must be aligned to their elements");
+  if (rows == 0 || n_heads == 0) return MT_OK;
+  Mrope a;
+  a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  a.y = reinterpret_cast<__nv_bfloat16*>(y);
+  a.pos = pos;
+  a.ld_x = ld_x;
+  a.ld_y = ld_y;
+  a.ld_pos = ld_pos;
+  a.rows = rows;
+  a.heads = n_heads;
+  a.d = head_dim;
+  a.pairs = static_cast<int>(pairs);
+  a.tile = 1;
+  a.sign = inverse ? -1.f : 1.f;
+  // axis and frequency of each pair: the axes' pairs in runs, or dealt out to the axes in turn
+  int used[MAX_AXES] = {0}, next = 0;
+  const double log_theta = std::log(static_cast<double>(theta)), turn = 6.283185307179586476925286766559;
+  for (int i = 0; i < a.pairs; ++i) {
+    while (used[next] == sections[next]) next = (next + 1) % n_axes;
+    const double expo = per_axis ? static_cast<double>(used[next]) / sections[next] : static_cast<double>(i) / a.pairs;
+    a.axis[i] = static_cast<uint8_t>(next);
+    a.turns[i] = std::exp(-expo * log_theta) / turn;
+    ++used[next];
+    if (interleaved) next = (next + 1) % n_axes;
+  }
+  for (int i = a.pairs; i < MAX_PAIRS; ++i) {
+    a.axis[i] = 0;
+    a.turns[i] = 0.0;
+  }
+  // the widest vector that divides the pairs and the head and keeps rows aligned
+  const uintptr_t all = bits | static_cast<uintptr_t>(ld_x) * 2 | static_cast<uintptr_t>(ld_y) * 2 |
+                        static_cast<uintptr_t>(a.pairs) * 2 | static_cast<uintptr_t>(head_dim) * 2;
+  const cudaStream_t st = as_stream(stream);
+  if (all % 16 == 0) return go<8>(a, st);
+  if (all % 8 == 0) return go<4>(a, st);
+  if (all % 4 == 0) return go<2>(a, st);
+  return go<1>(a, st);
+}

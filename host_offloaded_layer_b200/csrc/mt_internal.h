@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <atomic>
 #include <string>
 
 #include "mt.h"
@@ -45,6 +46,15 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 
 // Number of SMs of the current device (cached per device).
 int num_sms();
+
+// Lets a kernel use up to 224 KiB of dynamic shared memory, once on each device (one static object a kernel).
+class SmemOptIn {
+ public:
+  mt_status raise(const void* kernel);
+
+ private:
+  std::atomic<uint64_t> done_{0};  // bit d: device d
+};
 
 // Device error word set by bounded waits that ran out (one per device image).
 int32_t* device_error_word();

@@ -1,0 +1,1133 @@
+// Muon: momentum and orthogonalisation of a weight matrix's gradient by Newton-Schulz products.
+//
+//   m' = mu m + g, u = g + mu m' (Nesterov) or m', X = u / (|u|_F + eps)
+//   steps times: A = X X^T, X <- a X + (b A + c A^2) X; out = bf16(scale * X)
+//
+// with (a, b, c) = (3.4445, -4.7750, 2.0315), X on its short side (A = X^T X and X <- a X + X (b A + c A^2)
+// where the matrix is taller than wide: the tensor cores read either operand in either order, so nothing is
+// transposed). Written m <= n for the two sides, a step is m^2 n + m^3 + 2 m^2 n multiply-adds when the two
+// symmetric products compute only the tiles on and below the diagonal and store each twice.
+//
+// Number formats. The operands of the products are fp16, the sums fp32. bf16 operands, 8 bits, leave the
+// result 1-10% off. fp16 has 11 bits, and its range is enough because the singular values of X stay below
+// 1.2023 (the polynomial's maximum on [0, 1], which it maps into itself): X is held times 2^14, A (< 1.45)
+// times 2^14, b A + c A^2 (> -2.81) and the whole polynomial (<= 3.4445) times 2^13. What fp16 operands
+// would lose is the weak directions: their singular values grow by a factor of a each step, and so does the
+// rounding noise that the strong directions leave in their place. In the early steps a X is therefore added
+// from a two-term X (fp16 head + fp16 rest, 22 bits), while the products take the head alone: a rounding of
+// b A + c A^2 moves strong directions only, where nothing is amplified. In the last two steps, which amplify
+// little, the polynomial takes a on its diagonal and X its head only. Against the same steps in fp64 the
+// result is 1e-3 (2-norm) off before its rounding to bf16, which alone is 1.7e-3, for Gaussian matrices and
+// for a few strong directions over noise alike (64..4096 wide); fp16 throughout is up to 1.4e-2 off.
+// |u|_F is summed in fp64, so that no magnitude of g that fp32 holds over- or underflows.
+//
+// Matrices whose short side is at most 64 take no tensor cores: their Gram matrix (in fp64) is all that the
+// steps need, one CTA runs them on it in fp32, and the result is one product with u: three launches.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mt_internal.h"
+#include "tcgen05.cuh"
+
+namespace mt {
+namespace {
+
+using namespace tc;
+
+constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
+constexpr float S_X = 16384.f, S_A = 16384.f, S_P = 8192.f;
+constexpr int TINY = 64;  // the widest short side of the Gram path
+
+// ------------------------------------------------------------------ momentum, norm, head and rest of X
+struct Grad {
+  const float* g;
+  const float* m_in;  // NULL: u = g
+  float* m_out;
+  int64_t ld_g, ld_m, rows, cols;
+  float mu;
+  int nesterov;
+};
+
+// m' and u of one element from g and m (two roundings of fp32 each, as written).
+__device__ __forceinline__ float momentum_step(const Grad& p, float g, float m, float& mo) {
+  mo = fmaf(p.mu, m, g);
+  return p.nesterov ? fmaf(p.mu, mo, g) : mo;
+}
+
+constexpr int NORM_PARTS = 592;  // CTAs of the norm pass, each of which leaves one partial sum
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
+  __syncthreads();
+  return s;
+}
+
+// The passes over the matrix walk tiles of (256 / tx) * 8 rows and tx * VEC columns, tx a power of two that
+// fits narrow matrices, VEC = 4 where rows are 16-byte aligned.
+struct Walk {
+  int tx_log2;
+  int64_t col_tiles, tiles;
+};
+
+template <int VEC, class F>
+__device__ __forceinline__ void walk(const Walk& w, int64_t rows, int64_t cols, F&& f) {
+  const int tx = 1 << w.tx_log2, ty = 256 >> w.tx_log2;
+  const int x = threadIdx.x & (tx - 1), y = threadIdx.x >> w.tx_log2;
+  for (int64_t tl = blockIdx.x; tl < w.tiles; tl += gridDim.x) {
+    const int64_t rt = tl / w.col_tiles, ct = tl - rt * w.col_tiles;
+    const int64_t col = (ct * tx + x) * VEC;
+    if (col >= cols) continue;
+#pragma unroll 4
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = rt * (8 * ty) + k * ty + y;
+      if (row < rows) f(row, col);
+    }
+  }
+}
+
+template <int VEC>
+struct F32;
+template <>
+struct F32<4> {
+  using type = float4;
+};
+template <>
+struct F32<1> {
+  using type = float;
+};
+
+template <int VEC>
+__device__ __forceinline__ void ldv(float (&d)[VEC], const float* p) {
+  *reinterpret_cast<typename F32<VEC>::type*>(d) = *reinterpret_cast<const typename F32<VEC>::type*>(p);
+}
+
+// Writes m' and a partial |u|^2 (fp64) a CTA.
+template <int VEC>
+__global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* __restrict__ parts) {
+  double s = 0.0;
+  walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
+    float g[VEC], m[VEC];
+    ldv<VEC>(g, p.g + row * p.ld_g + col);
+    if (p.m_in) {
+      ldv<VEC>(m, p.m_in + row * p.ld_m + col);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        float mo;
+        g[i] = momentum_step(p, g[i], m[i], mo);
+        m[i] = mo;
+      }
+      *reinterpret_cast<typename F32<VEC>::type*>(p.m_out + row * p.ld_m + col) =
+          *reinterpret_cast<typename F32<VEC>::type*>(m);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s = fma(static_cast<double>(g[i]), static_cast<double>(g[i]), s);
+  });
+  s = block_sum(s);
+  if (threadIdx.x == 0) parts[blockIdx.x] = s;
+}
+
+// X = S_X u / (|u| + eps) as fp16 head and rest, from g and the m' that the norm pass left.
+template <int VEC>
+__global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* __restrict__ parts, int n_parts,
+                                                         double eps, __half* __restrict__ hi, __half* __restrict__ lo,
+                                                         int64_t ld_x) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n_parts; i += 256) s += parts[i];
+  s = block_sum(s);
+  // the factor as a mantissa and two powers of two: u times it stays in fp32's range for any |u|
+  int e;
+  const float mant = static_cast<float>(frexp(static_cast<double>(S_X) / (sqrt(s) + eps), &e));
+  const float p1 = ldexpf(1.f, e / 2), p2 = ldexpf(1.f, e - e / 2);
+  walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
+    float g[VEC], m[VEC];
+    if (!p.m_in || p.nesterov) ldv<VEC>(g, p.g + row * p.ld_g + col);
+    if (p.m_in) {
+      ldv<VEC>(m, p.m_out + row * p.ld_m + col);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) g[i] = p.nesterov ? fmaf(p.mu, m[i], g[i]) : m[i];
+    }
+    __half h[VEC], l[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float v = g[i] * mant * p1 * p2;
+      h[i] = __float2half_rn(v);
+      l[i] = __float2half_rn(v - __half2float(h[i]));
+    }
+    const int64_t at = row * ld_x + col;
+    if constexpr (VEC == 4) {
+      *reinterpret_cast<uint2*>(hi + at) = *reinterpret_cast<uint2*>(h);
+      if (lo) *reinterpret_cast<uint2*>(lo + at) = *reinterpret_cast<uint2*>(l);
+    } else {
+      hi[at] = h[0];
+      if (lo) lo[at] = l[0];
+    }
+  });
+}
+
+// ------------------------------------------------------------------ products
+// v = alpha * (A B^T)[r, c] + beta * (add_hi + add_lo)[r, c] + diag (r == c), stored as fp16 (head, and rest
+// where out_lo is set) or, where out_bf is set, as bf16. Internal matrices have rows of whole 64-element
+// groups, so 16-column chunks are always stored whole there.
+struct NsArgs {
+  int M, N, K;
+  int sym;     // square and symmetric: tiles on and below the diagonal only, each stored twice
+  int raster;  // 1: row blocks outer; 2: column blocks outer (the polynomial's matrix stays in L2)
+  float alpha, beta, diag;
+  const __half *add_hi, *add_lo;
+  __half *out_hi, *out_lo;
+  int64_t ld_add, ld_out;
+  __nv_bfloat16* out_bf;
+  int64_t ld_bf;
+  int bf_v16;  // out_bf rows hold 16-byte aligned chunks
+};
+
+__device__ __forceinline__ void ld32B(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32B(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ float2 h2f(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t f2h(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Epilogue of 16 columns of the 32 rows that a warp holds, one row a lane (all lanes call it).
+__device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, float (&v)[16], bool mirror) {
+  const bool live = row < e.M;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= e.alpha;
+  if (e.add_hi && live) {
+    uint32_t w[8];
+    const int64_t at = static_cast<int64_t>(row) * e.ld_add + col0;
+    ld32B(e.add_hi + at, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = h2f(w[i]);
+      v[2 * i] = fmaf(e.beta, f.x, v[2 * i]);
+      v[2 * i + 1] = fmaf(e.beta, f.y, v[2 * i + 1]);
+    }
+    if (e.add_lo) {
+      ld32B(e.add_lo + at, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = h2f(w[i]);
+        v[2 * i] = fmaf(e.beta, f.x, v[2 * i]);
+        v[2 * i + 1] = fmaf(e.beta, f.y, v[2 * i + 1]);
+      }
+    }
+  }
+  if (e.diag != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (row == col0 + i) v[i] += e.diag;
+  }
+  if (e.out_bf) {
+    if (!live) return;
+    __nv_bfloat16* o = e.out_bf + static_cast<int64_t>(row) * e.ld_bf + col0;
+    if (e.bf_v16 && col0 + 16 <= e.N) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint4 u;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
+        reinterpret_cast<uint4*>(o)[q] = u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (col0 + i < e.N) o[i] = __float2bfloat16_rn(v[i]);
+    }
+    return;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = f2h(v[2 * i], v[2 * i + 1]);
+  if (live) {
+    st32B(e.out_hi + static_cast<int64_t>(row) * e.ld_out + col0, w);
+    if (e.out_lo) {
+      uint32_t l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = h2f(w[i]);
+        l[i] = f2h(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+      }
+      st32B(e.out_lo + static_cast<int64_t>(row) * e.ld_out + col0, l);
+    }
+  }
+  if (mirror) {
+    // transposed: lanes exchange their neighbour's pair of columns, so that each stores two rows of one column
+    // (a pair (row, row + 1) that ends on the last row writes one element into the row's padding)
+    const bool odd = threadIdx.x & 1;
+    const int r2 = row & ~1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, w[i], 1);
+      const uint32_t t = odd ? __byte_perm(o, w[i], 0x7632) : __byte_perm(w[i], o, 0x5410);
+      const int c = col0 + 2 * i + (odd ? 1 : 0);
+      if (r2 < e.M && c < e.N) *reinterpret_cast<uint32_t*>(e.out_hi + static_cast<int64_t>(c) * e.ld_out + r2) = t;
+    }
+  }
+}
+
+// Tile t of the walk: of a symmetric matrix the t-th on or below the diagonal, row by row.
+__device__ __forceinline__ void ns_tile(const NsArgs& e, int t, int num_m, int num_n, int& mb, int& nb) {
+  if (e.sym) {
+    mb = static_cast<int>((sqrtf(8.f * static_cast<float>(t) + 1.f) - 1.f) * 0.5f);
+    while ((mb + 1) * (mb + 2) / 2 <= t) ++mb;
+    while (mb * (mb + 1) / 2 > t) --mb;
+    nb = t - mb * (mb + 1) / 2;
+  } else if (e.raster == 1) {
+    mb = t / num_n;
+    nb = t - mb * num_n;
+  } else {
+    nb = t / num_m;
+    mb = t - nb * num_m;
+  }
+}
+
+int ns_tiles(const NsArgs& e, int bm) {
+  const int num_m = (e.M + bm - 1) / bm, num_n = (e.N + bm - 1) / bm;
+  return e.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
+}
+
+constexpr int HALF = 128 * 64 * 2;    // 16 KiB: 128 rows of one operand, one 64-wide K atom
+constexpr int MN_BOX = 64 * 64 * 2;   // one 64 x 64 MN-major box
+constexpr int ATOMS = 6;              // K atoms of both operands that a CTA's ring holds: 192 KiB
+constexpr int RING = ATOMS * 2 * HALF;
+constexpr int SMEM_BYTES = RING + 256 + 1024;
+constexpr int NS_THREADS = 192;       // TMA warp, MMA warp, four epilogue warps
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// Instruction descriptor of kind::f16 with fp16 operands and fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Bytes that loading 128 rows of an operand from r0 brings for one K atom (boxes past its R rows are not loaded).
+__device__ __forceinline__ uint32_t rows_bytes(bool mn, int r0, int R) {
+  if (!mn) return r0 < R ? HALF : 0;
+  return (r0 < R ? MN_BOX : 0) + (r0 + 64 < R ? MN_BOX : 0);
+}
+
+// One K atom of 128 rows of an operand. K-major: a box of 64 (K) x 128 rows. MN-major: two boxes of 64 rows x
+// 64 (K), `mn_stride` bytes apart.
+template <bool MN, class Load>
+__device__ __forceinline__ void load_atom(uint32_t dst, int mn_stride, int r0, int R, int k, Load&& load) {
+  if (!MN) {
+    if (r0 < R) load(dst, k, r0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (r0 + 64 * j < R) load(dst + j * mn_stride, r0 + 64 * j, k);
+  }
+}
+
+// Descriptor of K step kk (16 wide) of a stage of KA atoms: K-major, atom kk / 4 and 32 bytes a step inside the
+// swizzled rows; MN-major, 16 rows of K (2 KiB) a step, the two 64-row halves KA boxes apart.
+template <bool MN, int KA>
+__device__ __forceinline__ uint64_t step_desc(uint32_t base, int kk) {
+  return MN ? smem_desc(base + kk * 2048, KA * MN_BOX, 1024)
+            : smem_desc(base + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024);
+}
+
+// ---------------------------------------------------------------- 256 x 256 tiles on two SMs
+// A persistent cluster of two CTAs: each stages its 128 rows of A and 128 columns of B, the even one issues
+// cta_group::2 products for both into one of two 256-column accumulators, and both drain theirs while the
+// next tile runs.
+template <bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
+    ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, NsArgs ep,
+                   int32_t* err) {
+  constexpr int KA = 2, STAGES = ATOMS / KA, OP_STAGE = HALF * KA, BK = 64 * KA;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * OP_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);  // TMA (both CTAs) -> MMA, in the even CTA
+  uint64_t* empty = full + STAGES;                            // MMA -> TMA, in each CTA
+  uint64_t* tfull = empty + STAGES;                           // MMA -> epilogue, in each CTA
+  uint64_t* tempty = tfull + 2;                               // epilogue warps of both CTAs -> MMA, in the even CTA
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const int num_m = (ep.M + 255) / 256, num_n = (ep.N + 255) / 256;
+  const int num_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
+  const int num_kb = (ep.K + BK - 1) / BK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&tfull[b]), 1);
+      mbar_init(smem_u32(&tempty[b]), 8);  // four epilogue warps of each CTA
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_sync();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = cluster; t < num_tiles && ok; t += n_clusters) {
+      int mb, nb;
+      ns_tile(ep, t, num_m, num_n, mb, nb);
+      const int m_own = mb * 256 + static_cast<int>(rank) * 128, n_own = nb * 256 + static_cast<int>(rank) * 128;
+      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        const int s = it % STAGES;
+        if (!warp_wait(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t fb = map_to_rank(smem_u32(&full[s]), 0);
+          const int k0 = kb * BK, atoms = min(KA, (ep.K - k0 + 63) / 64);
+          if (rank == 0) {
+            const uint32_t bytes = rows_bytes(A_MN, mb * 256, ep.M) + rows_bytes(A_MN, mb * 256 + 128, ep.M) +
+                                   rows_bytes(B_MN, nb * 256, ep.N) + rows_bytes(B_MN, nb * 256 + 128, ep.N);
+            mbar_expect_tx(smem_u32(&full[s]), bytes * static_cast<uint32_t>(atoms));
+          }
+          auto load = [&](const CUtensorMap* map) {
+            return [=](uint32_t dst, int c0, int c1) {
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                  "{%3, %4}], [%2];" ::"r"(dst),
+                  "l"(reinterpret_cast<uint64_t>(map)), "r"(fb), "r"(c0), "r"(c1)
+                  : "memory");
+            };
+          };
+          const uint32_t a_dst = smem_u32(sA + s * OP_STAGE), b_dst = smem_u32(sB + s * OP_STAGE);
+          for (int at = 0; at < atoms; ++at) {
+            load_atom<A_MN>(a_dst + at * (A_MN ? MN_BOX : HALF), KA * MN_BOX, m_own, ep.M, k0 + 64 * at, load(&tmA));
+            load_atom<B_MN>(b_dst + at * (B_MN ? MN_BOX : HALF), KA * MN_BOX, n_own, ep.N, k0 + 64 * at, load(&tmB));
+          }
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_f16(256, 256, A_MN, B_MN);
+      constexpr uint16_t both = 0x3;
+      auto commit = [&](uint64_t* bar) {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(both)
+            : "memory");
+      };
+      uint32_t it = 0;
+      int tl = 0;
+      bool ok = true;
+      for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++tl) {
+        const int ab = tl & 1;
+        if (!warp_wait(smem_u32(&tempty[ab]), ((tl >> 1) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) break;
+        fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(ab * 256);
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!warp_wait(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (lane == 0) {
+            const uint32_t a_base = smem_u32(sA + s * OP_STAGE), b_base = smem_u32(sB + s * OP_STAGE);
+            const int ksteps = 4 * min(KA, (ep.K - kb * BK + 63) / 64);
+            for (int kk = 0; kk < ksteps; ++kk)
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\t"
+                  "setp.ne.b32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                  "l"(step_desc<A_MN, KA>(a_base, kk)), "l"(step_desc<B_MN, KA>(b_base, kk)), "r"(idesc),
+                  "r"((kb > 0 || kk > 0) ? 1u : 0u));
+            commit(&empty[s]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) commit(&tfull[ab]);
+        __syncwarp();
+      }
+    }
+  } else {
+    const int q = warp & 3;  // TMEM lanes [32 q, 32 q + 32)
+    int tl = 0;
+    for (int t = cluster; t < num_tiles; t += n_clusters, ++tl) {
+      const int ab = tl & 1;
+      int mb, nb;
+      ns_tile(ep, t, num_m, num_n, mb, nb);
+      if (!warp_wait(smem_u32(&tfull[ab]), (tl >> 1) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE)) break;
+      fence_after();
+      const int row = mb * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * 256);
+      for (int c = 0; c < 8; ++c) {
+        const int col0 = nb * 256 + c * 32;
+        if (col0 >= ep.N) break;
+        uint32_t r[32];
+        tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (col0 + 16 * h >= ep.N) break;
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
+          finish16(ep, row, col0 + 16 * h, v, ep.sym && mb != nb);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         map_to_rank(smem_u32(&tempty[ab]), 0))
+                     : "memory");
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while its peer may still signal it
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
+}
+
+// ---------------------------------------------------------------- 128 x 128 tiles on one SM, K split over a cluster
+// For matrices with too few 256 x 256 tiles to fill the GPU: one tile a cluster of 1 to 8 CTAs, each of which
+// sums its share of K in its own TMEM. With more than one, the shares meet in shared memory: every CTA leaves its
+// fp32 tile there and each finishes 128 / size columns, adding the peers' tiles in rank order.
+constexpr int RED_LD = 132;  // floats of a row of the shared tile: 16-byte accesses of 8 rows hit 32 banks
+static_assert(128 * RED_LD * 4 <= RING, "the tile overlays the ring");
+
+template <bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(NS_THREADS, 1)
+    ns_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, NsArgs ep,
+                   int32_t* err) {
+  constexpr int STAGES = ATOMS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * HALF;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int num_m = (ep.M + 127) / 128, num_n = (ep.N + 127) / 128;
+  int mb, nb;
+  ns_tile(ep, static_cast<int>(blockIdx.x) / size, num_m, num_n, mb, nb);
+  const int atoms = (ep.K + 63) / 64;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * rank / size);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(atoms) * (rank + 1) / size);  // size <= atoms: never empty
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  bool done = true;  // this warp's waits all ended
+  if (warp == 0) {
+    const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int it = kb - kb0, s = it % STAGES;
+      if (!warp_wait(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
+      if (lane == 0) {
+        const uint32_t fb = smem_u32(&full[s]);
+        mbar_expect_tx(fb, bytes);
+        load_atom<A_MN>(smem_u32(sA + s * HALF), MN_BOX, mb * 128, ep.M, kb * 64,
+                        [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, &tmA, fb, c0, c1); });
+        load_atom<B_MN>(smem_u32(sB + s * HALF), MN_BOX, nb * 128, ep.N, kb * 64,
+                        [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, &tmB, fb, c0, c1); });
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int it = kb - kb0, s = it % STAGES;
+      if (!warp_wait(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      if (lane == 0) {
+        const uint32_t a_base = smem_u32(sA + s * HALF), b_base = smem_u32(sB + s * HALF);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(tmem_base, step_desc<A_MN, 1>(a_base, kk), step_desc<B_MN, 1>(b_base, kk), idesc,
+                    (it > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&empty[s]));
+      }
+      __syncwarp();
+    }
+    if (ok && lane == 0) umma_commit(smem_u32(tfull));
+    __syncwarp();
+  } else {
+    done = warp_wait(smem_u32(tfull), 0, abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
+    fence_after();
+    const int q = warp & 3, in_tile = q * 32 + lane;
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    if (done) {
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
+        if (size == 1) {
+          const int col0 = nb * 128 + c * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (col0 + 16 * h >= ep.N) break;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
+            finish16(ep, mb * 128 + in_tile, col0 + 16 * h, v, ep.sym && mb != nb);
+          }
+        } else {
+          // every product that read the ring has completed: the tile may overlay it
+          float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + in_tile * RED_LD + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            p[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                               __uint_as_float(r[4 * i + 3]));
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (size > 1) {
+    cluster_sync();
+    if (warp >= 2 && done) {
+      const int in_tile = (warp & 3) * 32 + lane, share = 128 / size;
+      for (int c = 0; c < share; c += 16) {
+        const int in_col = rank * share + c, col0 = nb * 128 + in_col;
+        if (col0 >= ep.N) break;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        const uint32_t at = smem_u32(smem) + (in_tile * RED_LD + in_col) * 4;
+        for (int p = 0; p < size; ++p) {
+          const uint32_t from = map_to_rank(at, static_cast<uint32_t>(p));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4 f;
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                         : "r"(from + 16 * i)
+                         : "memory");
+            v[4 * i] += f.x;
+            v[4 * i + 1] += f.y;
+            v[4 * i + 2] += f.z;
+            v[4 * i + 3] += f.w;
+          }
+        }
+        finish16(ep, mb * 128 + in_tile, col0, v, ep.sym && mb != nb);
+      }
+    }
+    cluster_sync();  // no CTA leaves while a peer reads its tile
+  }
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem_base) : "memory");
+}
+
+// An fp16 operand: element (r, k) at p[r * ld + k] (K-major) or p[k * ld + r] (MN-major).
+struct Operand {
+  const __half* p;
+  int64_t ld;
+  bool mn;
+  int64_t rows;
+};
+
+mt_status operand_map(CUtensorMap* m, const Operand& o, int64_t K) {
+  return o.mn ? tma_map_2d(m, o.p, o.rows, K, o.ld, 64, 64) : tma_map_2d(m, o.p, K, o.rows, o.ld, 64, 128);
+}
+
+// Clusters of two that run at once: one CTA an SM.
+int pair_clusters() { return std::max(1, num_sms() / 2); }
+
+template <bool A_MN, bool B_MN>
+mt_status ns_launch(const CUtensorMap& ta, const CUtensorMap& tb, const NsArgs& e, int split, cudaStream_t st) {
+  int32_t* err = device_error_word();
+  if (!err) return fail(MT_ERR_CUDA, "device error word unavailable");
+  if (split == 0) {
+    static SmemOptIn opt;
+    MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_pair_kernel<A_MN, B_MN>)));
+    const int clusters = std::min(ns_tiles(e, 256), pair_clusters());
+    ns_pair_kernel<A_MN, B_MN><<<2 * clusters, NS_THREADS, SMEM_BYTES, st>>>(ta, tb, e, err);
+    return launch_check("ns_pair_kernel");
+  }
+  static SmemOptIn opt;
+  MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_tile_kernel<A_MN, B_MN>)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ns_tiles(e, 128) * split, 1, 1);
+  cfg.blockDim = dim3(NS_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MT_CUDA(cudaLaunchKernelEx(&cfg, ns_tile_kernel<A_MN, B_MN>, ta, tb, e, err));
+  return launch_check("ns_tile_kernel");
+}
+
+// 0: 256 x 256 tiles on SM pairs; else 128 x 128 tiles with K split over that many CTAs.
+int pick_split(const NsArgs& e) {
+  const int sms = num_sms();
+  if (ns_tiles(e, 256) * 2 >= sms / 2) return 0;
+  const int tiles = ns_tiles(e, 128), atoms = (e.K + 63) / 64;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= sms && atoms >= split * 4) split *= 2;
+  return split;
+}
+
+mt_status ns_product(const Operand& a, const Operand& b, const NsArgs& e, cudaStream_t st) {
+  CUtensorMap ta, tb;
+  MT_TRY(operand_map(&ta, a, e.K));
+  MT_TRY(operand_map(&tb, b, e.K));
+  const int split = pick_split(e);
+  add_exec_flops(2.0 * double(e.M) * double(e.N) * double(e.K) * (e.sym ? 0.5 : 1.0));
+  if (!a.mn && !b.mn) return ns_launch<false, false>(ta, tb, e, split, st);
+  if (!a.mn) return ns_launch<false, true>(ta, tb, e, split, st);
+  return ns_launch<true, true>(ta, tb, e, split, st);
+}
+
+// ------------------------------------------------------------------ short side of at most 64
+// u of the element k on the long side, i on the short one.
+struct TinyArgs {
+  Grad p;
+  int64_t n;   // long side
+  int m;       // short side
+  int tall;    // rows are the long side
+  int steps;
+  float scale;
+  double eps;
+  double* gram;   // [parts][m * m]
+  int parts;
+  float* r;       // [m * m]
+  __nv_bfloat16* o;
+  int64_t ld_o;
+};
+
+constexpr int CHUNK = 64;  // long-side elements a CTA holds at a time
+
+// u[k][i] of a chunk from k0 into shared memory (rows of 65); first: also writes m'.
+__device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, float (*u)[TINY + 1], bool first) {
+  const int kn = static_cast<int>(min(static_cast<int64_t>(CHUNK), a.n - k0));
+  for (int e = threadIdx.x; e < CHUNK * TINY; e += 256) {
+    const int k = a.tall ? e / TINY : e % CHUNK, i = a.tall ? e % TINY : e / CHUNK;  // global memory's order
+    float v = 0.f;
+    if (k < kn && i < a.m) {
+      const int64_t row = a.tall ? k0 + k : i, col = a.tall ? i : k0 + k;
+      v = !a.p.m_in || first || a.p.nesterov ? a.p.g[row * a.p.ld_g + col] : 0.f;
+      if (a.p.m_in) {
+        const int64_t at = row * a.p.ld_m + col;
+        if (first) {
+          float mo;
+          v = momentum_step(a.p, v, a.p.m_in[at], mo);
+          a.p.m_out[at] = mo;
+        } else {
+          v = a.p.nesterov ? fmaf(a.p.mu, a.p.m_out[at], v) : a.p.m_out[at];
+        }
+      }
+    }
+    u[k][i] = v;
+  }
+}
+
+// Partial Gram matrices u u^T in fp64, 4 x 4 of them a thread.
+__global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
+  __shared__ float u[CHUNK][TINY + 1];
+  double acc[4][4] = {};
+  const int ti = threadIdx.x & 15, tj = threadIdx.x >> 4;
+  const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    __syncthreads();
+    tiny_chunk(a, c * CHUNK, u, true);
+    __syncthreads();
+    if (ti * 4 < a.m && tj * 4 < a.m) {
+      for (int k = 0; k < CHUNK; ++k) {
+        double x[4], y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x[q] = u[k][ti * 4 + q];
+          y[q] = u[k][tj * 4 + q];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fma(x[i], y[j], acc[i][j]);
+      }
+    }
+  }
+  double* out = a.gram + static_cast<int64_t>(blockIdx.x) * a.m * a.m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = ti * 4 + i, s = tj * 4 + j;
+      if (r < a.m && s < a.m) out[r * a.m + s] = acc[i][j];
+    }
+}
+
+// c = sa * a b + sd * I, 64 x 64 matrices with rows of 65, 2 x 2 elements a thread of 1024 (32 x 32).
+__device__ __forceinline__ void mul64(float (*c)[TINY + 1], float (*a)[TINY + 1], float (*b)[TINY + 1], float sa, int m) {
+  const int i = (threadIdx.x >> 5) * 2, j = threadIdx.x & 31;
+  float s[2][2] = {};
+  if (i < m) {
+    for (int k = 0; k < m; ++k) {
+      const float x0 = a[i][k], x1 = a[i + 1][k], y0 = b[k][j], y1 = b[k][j + 32];
+      s[0][0] = fmaf(x0, y0, s[0][0]);
+      s[0][1] = fmaf(x0, y1, s[0][1]);
+      s[1][0] = fmaf(x1, y0, s[1][0]);
+      s[1][1] = fmaf(x1, y1, s[1][1]);
+    }
+  }
+  __syncthreads();  // c may be a or b
+  c[i][j] = sa * s[0][0];
+  c[i][j + 32] = sa * s[0][1];
+  c[i + 1][j] = sa * s[1][0];
+  c[i + 1][j + 32] = sa * s[1][1];
+  __syncthreads();
+}
+
+// The steps on the Gram matrix: with P = a I + b A + c A^2, Q <- P Q, A <- P A P. r = scale * Q / (|u| + eps).
+__global__ void __launch_bounds__(1024) muon_tiny_steps_kernel(TinyArgs a) {
+  extern __shared__ float tiny_smem[];
+  float(*A)[TINY + 1] = reinterpret_cast<float(*)[TINY + 1]>(tiny_smem);
+  float(*P)[TINY + 1] = A + TINY;
+  float(*Q)[TINY + 1] = P + TINY;
+  __shared__ double trace[TINY];
+  const int mm = a.m * a.m;
+  double own[4];  // at most 4 elements of the Gram matrix a thread
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = threadIdx.x + q * 1024;
+    double s = 0.0;
+    if (e < mm)
+      for (int p = 0; p < a.parts; ++p) s += a.gram[static_cast<int64_t>(p) * mm + e];
+    own[q] = s;
+    if (e < mm && e / a.m == e % a.m) trace[e / a.m] = s;
+  }
+  for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
+    A[e / TINY][e % TINY] = 0.f;
+    Q[e / TINY][e % TINY] = e / TINY == e % TINY ? 1.f : 0.f;
+  }
+  __syncthreads();
+  double sum = 0.0;
+  for (int i = 0; i < a.m; ++i) sum += trace[i];
+  const double norm = sqrt(sum) + a.eps;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = threadIdx.x + q * 1024;
+    if (e < mm) A[e / a.m][e % a.m] = static_cast<float>(own[q] / norm / norm);
+  }
+  __syncthreads();
+  for (int st = 0; st < a.steps; ++st) {
+    mul64(P, A, A, NS_C, a.m);
+    for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
+      const int i = e / TINY, j = e % TINY;
+      P[i][j] += NS_B * A[i][j] + (i == j ? NS_A : 0.f);
+    }
+    __syncthreads();
+    mul64(Q, P, Q, 1.f, a.m);
+    if (st + 1 < a.steps) {
+      mul64(A, P, A, 1.f, a.m);
+      mul64(A, A, P, 1.f, a.m);
+    }
+  }
+  const double f = static_cast<double>(a.scale) / norm;
+  for (int e = threadIdx.x; e < mm; e += 1024) a.r[e] = static_cast<float>(Q[e / a.m][e % a.m] * f);
+}
+
+// o = r u, a chunk of the long side a CTA.
+__global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
+  __shared__ float u[CHUNK][TINY + 1];
+  __shared__ float r[TINY][TINY + 1];
+  for (int e = threadIdx.x; e < TINY * TINY; e += 256) {
+    const int i = e / TINY, j = e % TINY;
+    r[i][j] = i < a.m && j < a.m ? a.r[i * a.m + j] : 0.f;
+  }
+  const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
+  // neighbouring threads write neighbouring elements of a row of o: along the short side of a tall matrix, the long
+  // side of a wide one; 16 elements a thread, every fourth of the other side
+  const int fast = threadIdx.x & 63, slow = threadIdx.x >> 6;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    __syncthreads();
+    tiny_chunk(a, c * CHUNK, u, false);
+    __syncthreads();
+    float s[16] = {};
+    for (int j = 0; j < a.m; ++j) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int k = a.tall ? slow + 4 * q : fast, i = a.tall ? fast : slow + 4 * q;
+        s[q] = fmaf(r[i][j], u[k][j], s[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int k = a.tall ? slow + 4 * q : fast, i = a.tall ? fast : slow + 4 * q;
+      const int64_t lk = c * CHUNK + k;
+      if (lk < a.n && i < a.m)
+        a.o[a.tall ? lk * a.ld_o + i : static_cast<int64_t>(i) * a.ld_o + lk] = __float2bfloat16_rn(s[q]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ workspace
+struct Plan {
+  int64_t m, n, ld_x, ld_a;
+  int parts;
+  double* part;
+  __half *hi[2], *lo, *A, *P;
+  double* gram;
+  float* r;
+  uint64_t bytes;
+};
+
+Plan plan(int64_t rows, int64_t cols, void* ws) {
+  Plan p = {};
+  p.m = std::min(rows, cols);
+  p.n = std::max(rows, cols);
+  Bump b(ws, ~0ull);
+  if (p.m <= TINY) {
+    p.parts = static_cast<int>(std::min<int64_t>(148, (p.n + CHUNK - 1) / CHUNK));
+    p.gram = b.take<double>(static_cast<int64_t>(p.parts) * p.m * p.m);
+    p.r = b.take<float>(p.m * p.m);
+  } else {
+    p.parts = NORM_PARTS;
+    p.ld_x = align_up(cols, 64);
+    p.ld_a = align_up(p.m, 64);
+    p.part = b.take<double>(NORM_PARTS);
+    for (auto& h : p.hi) h = b.take<__half>(rows * p.ld_x);
+    p.lo = b.take<__half>(rows * p.ld_x);
+    p.A = b.take<__half>(p.m * p.ld_a);
+    p.P = b.take<__half>(p.m * p.ld_a);
+  }
+  p.bytes = b.used;
+  return p;
+}
+
+Walk make_walk(int64_t rows, int64_t cols, int vec) {
+  Walk w;
+  w.tx_log2 = 8;
+  while (w.tx_log2 > 0 && (int64_t(1) << (w.tx_log2 - 1)) * vec >= cols) --w.tx_log2;
+  const int64_t width = (int64_t(1) << w.tx_log2) * vec, height = (256 >> w.tx_log2) * 8;
+  w.col_tiles = (cols + width - 1) / width;
+  w.tiles = w.col_tiles * ((rows + height - 1) / height);
+  return w;
+}
+
+mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
+  TinyArgs a;
+  a.p = g;
+  a.n = p.n;
+  a.m = static_cast<int>(p.m);
+  a.tall = g.rows > g.cols;
+  a.steps = c.steps;
+  a.scale = c.scale;
+  a.eps = c.eps;
+  a.gram = p.gram;
+  a.parts = p.parts;
+  a.r = p.r;
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  a.ld_o = ld_o;
+  muon_tiny_gram_kernel<<<p.parts, 256, 0, st>>>(a);
+  MT_TRY(launch_check("muon_tiny_gram_kernel"));
+  static SmemOptIn opt;
+  MT_TRY(opt.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel)));
+  muon_tiny_steps_kernel<<<1, 1024, 3 * TINY * (TINY + 1) * 4, st>>>(a);
+  MT_TRY(launch_check("muon_tiny_steps_kernel"));
+  const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
+  muon_tiny_apply_kernel<<<static_cast<unsigned>(std::min<int64_t>(chunks, 4 * num_sms())), 256, 0, st>>>(a);
+  return launch_check("muon_tiny_apply_kernel");
+}
+
+mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
+  const bool tall = g.rows > g.cols;
+  auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool v4 = g.cols % 4 == 0 && g.ld_g % 4 == 0 && a16(g.g) &&
+                  (!g.m_in || (g.ld_m % 4 == 0 && a16(g.m_in) && a16(g.m_out)));
+  const Walk w = make_walk(g.rows, g.cols, v4 ? 4 : 1);
+  const int parts = static_cast<int>(std::min<int64_t>(w.tiles, NORM_PARTS));
+  // a two-term X for all steps but the last two
+  const int two_term = c.steps - 2;
+  __half* lo = two_term > 0 ? p.lo : nullptr;
+  if (v4) {
+    muon_norm_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part);
+    MT_TRY(launch_check("muon_norm_kernel"));
+    muon_scale_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part, parts, c.eps, p.hi[0], lo, p.ld_x);
+  } else {
+    muon_norm_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part);
+    MT_TRY(launch_check("muon_norm_kernel"));
+    muon_scale_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part, parts, c.eps, p.hi[0], lo, p.ld_x);
+  }
+  MT_TRY(launch_check("muon_scale_kernel"));
+  const int m = static_cast<int>(p.m), n = static_cast<int>(p.n);
+  const Operand sq_a{p.A, p.ld_a, false, p.m}, sq_p{p.P, p.ld_a, false, p.m};
+  for (int s = 0; s < c.steps; ++s) {
+    const bool fold = s >= two_term, last = s + 1 == c.steps;
+    const __half* x = p.hi[s & 1];
+    // A = X X^T (X^T X): the short side's rows of X are K-major in a wide matrix, MN-major in a tall one
+    NsArgs e = {};
+    const Operand short_side{x, p.ld_x, tall, p.m};
+    e.M = e.N = m;
+    e.K = n;
+    e.sym = 1;
+    e.alpha = S_A / (S_X * S_X);
+    e.out_hi = p.A;
+    e.ld_out = p.ld_a;
+    MT_TRY(ns_product(short_side, short_side, e, st));
+    // P = b A + c A^2 (+ a I)
+    e.K = m;
+    e.alpha = NS_C * S_P / (S_A * S_A);
+    e.beta = NS_B * S_P / S_A;
+    e.diag = fold ? NS_A * S_P : 0.f;
+    e.add_hi = p.A;
+    e.ld_add = p.ld_a;
+    e.out_hi = p.P;
+    MT_TRY(ns_product(sq_a, sq_a, e, st));
+    // X' = P X (+ a X), the long side of X as rows: MN-major in a wide matrix, K-major in a tall one
+    e = {};
+    const Operand long_side{x, p.ld_x, !tall, p.n};
+    e.M = tall ? n : m;
+    e.N = tall ? m : n;
+    e.K = m;
+    e.raster = tall ? 1 : 2;
+    e.alpha = (last ? c.scale / S_X : 1.f) / S_P;
+    if (!fold) {
+      e.beta = NS_A;
+      e.add_hi = x;
+      e.add_lo = p.lo;
+      e.ld_add = p.ld_x;
+    }
+    if (last) {
+      e.out_bf = reinterpret_cast<__nv_bfloat16*>(o);
+      e.ld_bf = ld_o;
+      e.bf_v16 = a16(o) && ld_o % 8 == 0;
+    } else {
+      e.out_hi = p.hi[(s + 1) & 1];
+      e.out_lo = s + 1 < two_term ? p.lo : nullptr;
+      e.ld_out = p.ld_x;
+    }
+    MT_TRY(tall ? ns_product(long_side, sq_p, e, st) : ns_product(sq_p, long_side, e, st));
+  }
+  return MT_OK;
+}
+
+}  // namespace
+}  // namespace mt
+
+using namespace mt;
+
+extern "C" {
+
+uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || rows >= (1ll << 31) || cols >= (1ll << 31)) return 0;
+  return plan(rows, cols, nullptr).bytes;
+}
+
+mt_status mt_muon_update(const float* g, int64_t ld_g, const float* m_in, float* m_out, int64_t ld_m, mt_bf16* o,
+                         int64_t ld_o, int64_t rows, int64_t cols, const mt_muon_cfg* cfg, void* ws, uint64_t ws_bytes,
+                         void* stream) {
+  const bool empty = rows == 0 || cols == 0;
+  if (!cfg || (!empty && (!g || !o))) return fail(MT_ERR_INVALID_ARG, "muon_update: NULL pointer");
+  if (!m_in != !m_out) return fail(MT_ERR_INVALID_ARG, "muon_update: m_in and m_out go together");
+  if (rows < 0 || cols < 0 || rows >= (1ll << 31) || cols >= (1ll << 31))
+    return fail(MT_ERR_INVALID_ARG, "muon_update: need 0 <= rows, cols < 2^31");
+  if (ld_g < cols || ld_o < cols || (m_in && ld_m < cols))
+    return fail(MT_ERR_INVALID_ARG, "muon_update: row stride smaller than cols");
+  if (cfg->steps < 1 || cfg->steps > 100) return fail(MT_ERR_INVALID_ARG, "muon_update: 1 to 100 steps, got %d", cfg->steps);
+  if (!std::isfinite(cfg->momentum) || !std::isfinite(cfg->scale) || !(cfg->eps > 0.f) || !std::isfinite(cfg->eps))
+    return fail(MT_ERR_INVALID_ARG, "muon_update: momentum and scale must be finite, eps positive and finite");
+  const uintptr_t f32 = reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(m_in) | reinterpret_cast<uintptr_t>(m_out);
+  if ((f32 & 3) || (reinterpret_cast<uintptr_t>(o) & 1))
+    return fail(MT_ERR_ALIGNMENT, "muon_update: pointers must be aligned to their elements");
+  if (empty) return MT_OK;
+  if (!ws) return fail(MT_ERR_INVALID_ARG, "muon_update: NULL workspace");
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(MT_ERR_ALIGNMENT, "muon_update: workspace must be 256-byte aligned");
+  const Plan p = plan(rows, cols, ws);
+  if (ws_bytes < p.bytes) return fail(MT_ERR_WORKSPACE, "muon_update: workspace too small");
+  Grad gr;
+  gr.g = g;
+  gr.m_in = m_in;
+  gr.m_out = m_out;
+  gr.ld_g = ld_g;
+  gr.ld_m = ld_m;
+  gr.rows = rows;
+  gr.cols = cols;
+  gr.mu = cfg->momentum;
+  gr.nesterov = cfg->nesterov != 0;
+  return p.m <= TINY ? muon_tiny(gr, *cfg, o, ld_o, p, as_stream(stream))
+                     : muon_general(gr, *cfg, o, ld_o, p, as_stream(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,106 @@
+// bf16 rows in vectors of 8, 4, 2 or 1 elements (the widest that a row's alignment allows), and warp sums of a
+// few values at once.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace mt {
+namespace vec {
+
+template <int VEC>
+struct Raw;
+template <>
+struct Raw<8> {
+  using type = uint4;
+};
+template <>
+struct Raw<4> {
+  using type = uint2;
+};
+template <>
+struct Raw<2> {
+  using type = uint32_t;
+};
+template <>
+struct Raw<1> {
+  using type = uint16_t;
+};
+
+__device__ __forceinline__ float2 bf2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void unpack(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = bf2(w[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint2& u, float* f) {
+  const float2 t = bf2(u.x), v = bf2(u.y);
+  f[0] = t.x;
+  f[1] = t.y;
+  f[2] = v.x;
+  f[3] = v.y;
+}
+__device__ __forceinline__ void unpack(const uint32_t& u, float* f) {
+  const float2 t = bf2(u);
+  f[0] = t.x;
+  f[1] = t.y;
+}
+__device__ __forceinline__ void unpack(const uint16_t& u, float* f) { f[0] = __uint_as_float(uint32_t(u) << 16); }
+
+__device__ __forceinline__ void pack(uint4& u, const float* f) {
+  u = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+__device__ __forceinline__ void pack(uint2& u, const float* f) { u = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3])); }
+__device__ __forceinline__ void pack(uint32_t& u, const float* f) { u = pack2(f[0], f[1]); }
+__device__ __forceinline__ void pack(uint16_t& u, const float* f) { u = __bfloat16_as_ushort(__float2bfloat16_rn(f[0])); }
+
+__device__ __forceinline__ void zero(uint4& u) { u = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void zero(uint32_t& u) { u = 0u; }
+__device__ __forceinline__ void zero(uint16_t& u) { u = 0; }
+
+// Sums of N values (N = 1, 2 or 4) over the warp, left in every lane. The first log2(N) exchanges halve the
+// number of values a lane carries, so N = 4 takes 10 shuffles instead of 20; the order of additions is fixed.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  constexpr unsigned ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  float s;
+  if constexpr (N == 4) {
+    const bool hi = lane & 16;
+    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(ALL, hi ? v[0] : v[2], 16);
+    const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(ALL, hi ? v[1] : v[3], 16);
+    const bool h2 = lane & 8;
+    s = (h2 ? b : a) + __shfl_xor_sync(ALL, h2 ? a : b, 8);
+  } else if constexpr (N == 2) {
+    const bool hi = lane & 16;
+    s = (hi ? v[1] : v[0]) + __shfl_xor_sync(ALL, hi ? v[0] : v[1], 16);
+    s += __shfl_xor_sync(ALL, s, 8);
+  } else {
+    s = v[0] + __shfl_xor_sync(ALL, v[0], 16);
+    s += __shfl_xor_sync(ALL, s, 8);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(ALL, s, o);
+  if constexpr (N == 1) {
+    v[0] = s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(ALL, s, i * (32 / N));
+  }
+}
+
+}  // namespace vec
+}  // namespace mt

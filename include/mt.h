@@ -205,6 +205,33 @@ mt_status mt_rmsnorm_bwd(const mt_bf16* dy, const mt_bf16* x, const mt_bf16* g, 
 mt_status mt_rmsnorm_bwd_noalloc(const mt_bf16* dy, const mt_bf16* x, const mt_bf16* g, const float* rstd,
                                  const mt_bf16* dres, mt_bf16* dx, float* dg, int64_t rows, int32_t H, void* stream);
 
+/* LayerNorm forward over rows of H (any H >= 1): mean = sum x / H, rstd =
+ * 1/sqrt(sum (x - mean)^2 / H + eps), y = (x - mean) * rstd * g + b. x and y are
+ * [rows] of H elements, ld_x and ld_y elements apart; what lies between H and
+ * the row stride is neither read nor written. g, b (bf16 [H]) and mean, rstd
+ * (fp32 [rows] out, what the backward needs) may each be NULL. y may be x (same
+ * row stride); they must not overlap otherwise. Pointers need the alignment of
+ * their elements only; 16-byte aligned rows (pointers and strides of 8
+ * elements, H a multiple of 8) are faster. H above 2^28: MT_ERR_UNSUPPORTED. */
+mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, const mt_bf16* b, mt_bf16* y,
+                           int64_t ld_y, float* mean, float* rstd, int64_t rows, int32_t H, float eps, void* stream);
+
+/* Bytes of workspace mt_layernorm_bwd needs (fixed-order partial sums of dg
+ * and db); 0 for sizes that the call refuses. */
+uint64_t mt_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H);
+
+/* LayerNorm backward: with xh = (x - mean) * rstd and w = dy * g,
+ * dx = rstd * (w - mean_j(w) - xh * mean_j(w xh)) + dres (dres may be NULL),
+ * dg[j] = sum_rows dy xh, db[j] = sum_rows dy (fp32 [H], fixed summation order,
+ * overwritten; each may be NULL; zeros for rows = 0). mean, rstd: of the
+ * forward. g may be NULL (a gain of 1). Rows as in mt_layernorm_fwd, each with
+ * a stride of its own. dx may be dy or dres (same row stride). ws: device, 16-byte
+ * aligned, not shared with a call that may run at the same time. */
+mt_status mt_layernorm_bwd(const mt_bf16* dy, int64_t ld_dy, const mt_bf16* x, int64_t ld_x, const mt_bf16* g,
+                           const float* mean, const float* rstd, const mt_bf16* dres, int64_t ld_dres, mt_bf16* dx,
+                           int64_t ld_dx, float* dg, float* db, int64_t rows, int32_t H, void* ws, uint64_t ws_bytes,
+                           void* stream);
+
 /* Rotate-half RoPE in place on the first n_heads heads (of head_dim d) of each
  * row of x (row stride ld elements; rows are [B, T], position = t). Pair
  * (i, i+d/2) rotates by t*theta^(-2i/d); inverse = 1 rotates by the negative
@@ -212,6 +239,29 @@ mt_status mt_rmsnorm_bwd_noalloc(const mt_bf16* dy, const mt_bf16* x, const mt_b
  * formed in fp64, the rotation is done in fp32. */
 mt_status mt_rope(mt_bf16* x, int64_t ld, int32_t B, int32_t T, int32_t n_heads, int32_t head_dim,
                   float theta, int32_t inverse, void* stream);
+
+/* Rotary positions with several axes (time, height, width of image and video
+ * tokens): rotate-half RoPE whose pairs take their position from one of n_axes
+ * (1 to 8). pos: device int32 [n_axes][rows], axes ld_pos elements apart (any
+ * value, negative too). sections: host array, the number of pairs of each axis;
+ * their sum P (at most head_dim / 2 and 128) pairs (i, i + P) of every head
+ * rotate by the angle pos[axis(i)][row] * omega_i, and the columns from 2P to
+ * head_dim are copied.
+ *   interleaved = 0: the pairs of axis 0 first, then those of axis 1, ...;
+ *   1: the pairs are dealt out to the axes in turn, skipping axes with none left.
+ *   per_axis = 0: omega_i = theta^(-i/P); 1: a ladder for each axis,
+ *   theta^(-j/sections[axis]) for the axis's j-th pair.
+ * inverse = 1 rotates by the negative angle (the adjoint, for the backward).
+ * x, y: rows ld_x / ld_y elements apart, n_heads heads of head_dim at the start
+ * of each; columns behind the heads are neither read nor written. y may be x
+ * (same row stride; only the rotated columns are then written); they must not
+ * overlap otherwise. Angles are reduced to a fraction of a turn in fp64, the
+ * rotation is done in fp32. Pointers need the alignment of their elements only;
+ * 16-byte aligned heads (pointers, strides, head_dim and P multiples of 8) are
+ * faster. */
+mt_status mt_mrope(const mt_bf16* x, int64_t ld_x, mt_bf16* y, int64_t ld_y, const int32_t* pos, int64_t ld_pos,
+                   const int32_t* sections, int32_t n_axes, int64_t rows, int32_t n_heads, int32_t head_dim,
+                   float theta, int32_t interleaved, int32_t per_axis, int32_t inverse, void* stream);
 
 /* SwiGLU forward: gu is [rows, 2F] (gate in columns [0,F), up in [F,2F));
  * m[r, j] = silu(g) * u, m is [rows, F]. */
@@ -456,6 +506,43 @@ mt_status mt_host_optimizer_create(mt_host_store* store, const mt_adamw_cfg* cfg
  * a mismatched layer or record size. */
 int32_t mt_host_optimizer_sink(int32_t layer, const float* host_slab, uint64_t n_elems, void* user);
 void mt_host_optimizer_destroy(mt_host_optimizer* o);
+
+/* ------------------------------------------------------------------------ */
+/* Muon (momentum and orthogonalisation of a matrix's gradient, on the GPU)  */
+/* ------------------------------------------------------------------------ */
+
+typedef struct mt_muon_cfg {
+  float momentum;    /* mu */
+  int32_t nesterov;  /* 1: u = g + mu m', 0: u = m' */
+  int32_t steps;     /* Newton-Schulz steps, 1 to 100 (5 is usual) */
+  float eps;         /* added to the norm, > 0 */
+  float scale;       /* factor of the result (1, or the update's learning-rate scale) */
+} mt_muon_cfg;
+
+/* Bytes of workspace mt_muon_update needs for a rows x cols matrix; 0 for sizes
+ * that it refuses and for an empty one. */
+uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols);
+
+/* The Muon update of one weight matrix from its fp32 gradient g (rows ld_g
+ * elements apart, e.g. a block of the gradient record of mt_layer_recompute_bwd):
+ *   m' = mu m + g, u = g + mu m' or m' (nesterov), X = u / (|u|_F + eps),
+ *   steps times: X <- a X + (b A + c A^2) X with A = X X^T and
+ *   (a, b, c) = (3.4445, -4.7750, 2.0315); o = bf16(scale X).
+ * m_in, m_out: fp32 momentum, rows ld_m elements apart; m_out may be m_in (the
+ * buffer is then updated in place); both NULL: u = g. o: bf16, rows ld_o
+ * elements apart, the direction to take off the weights. A matrix taller than
+ * wide uses A = X^T X. The products run on the tensor cores in fp16 with fp32
+ * sums (short sides of at most 64: fp32); before its rounding to bf16 the result
+ * is within about 2e-3 (2-norm) of the same steps in fp64 for 5 steps. Elements
+ * between cols and a row's stride are neither read nor written. A g or m that
+ * holds infinities or NaN gives NaN. Deterministic: fixed order of every sum.
+ * g, m_in, m_out, o: aligned to their elements (16-byte aligned rows of 4
+ * elements, 8 for o, are faster), none overlapping another but m_in = m_out.
+ * ws: device, 256-byte aligned, not shared with a call that may run at the same
+ * time. Asynchronous on stream. */
+mt_status mt_muon_update(const float* g, int64_t ld_g, const float* m_in, float* m_out, int64_t ld_m, mt_bf16* o,
+                         int64_t ld_o, int64_t rows, int64_t cols, const mt_muon_cfg* cfg, void* ws, uint64_t ws_bytes,
+                         void* stream);
 
 /* Host-side schedule (no CUDA): for n_layers and interval K, the sequence of
  * layer uses in compute order and, for a pool of n_slots weight buffers, the
