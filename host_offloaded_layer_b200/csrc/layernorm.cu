@@ -4,12 +4,23 @@
 //   w = dy g, dx = rstd (w - mean_j(w) - xh mean_j(w xh)) + dres, dg = sum_rows dy xh, db = sum_rows dy
 //
 // Both are bound by HBM: the forward has to move 4 bytes an element, the backward 6 (8 with dres). So every
-// element is read once: a group of W warps holds a whole row in registers (EPT elements a thread), which
-// also lets the variance be taken of x - mean (a second sum over registers, exact for rows whose mean is
-// large against their spread). The backward's column sums dg and db come from the same pass: a thread owns
-// the same columns of every row its group visits and keeps their sums in registers; a group adds its sums
-// to the CTA's in shared memory, a CTA leaves one partial row, and a second small kernel adds the partial
-// rows in a fixed order. No atomics: the result depends on the sizes alone.
+// element is read once: a group of W warps holds a whole row in registers, which also lets the variance be
+// taken of x - mean (a second sum over registers, exact for rows whose mean is large against their spread).
+// The backward's column sums dg and db come from the same pass: a thread owns the same columns of every row
+// its group visits and keeps their sums in registers; a group adds its sums to the CTA's in shared memory, a
+// CTA leaves one partial row, and a second small kernel adds the partial rows in a fixed order. No atomics:
+// the result depends on the sizes alone.
+//
+// Rows come through a ring in shared memory that cp.async fills some rows ahead; a thread copies exactly the
+// 16-byte vectors that it reads, so the ring needs no barrier, and what is in flight does not cost registers.
+// The arithmetic is packed (two fp32 a register pair): unpacked, the forward was bound by instruction issue
+// (72% of the slots at 2.2 TB/s of reads).
+//
+// Rows of any alignment take this path. A group's vectors are the 16-byte granules of memory that its rows
+// cover; where H or the row stride is odd, rows start at different places in their first granule, and that
+// place (`shift`, in elements) repeats every 8 rows: groups step by multiples of 8 rows, so that each sees one
+// shift and its threads keep their columns. The first and last vector of a row may be partial. (Only operands
+// whose rows lie differently in their granules go an element at a time.)
 #include <algorithm>
 
 #include "mt_internal.h"
@@ -21,8 +32,8 @@ namespace {
 using namespace vec;
 
 constexpr int SMS = 148;            // the partial rows of dg and db are counted for a whole B200, so that sums do not depend on the device
-constexpr int GROUP_THREADS = 256;  // groups of few warps share a CTA of about this size
-constexpr int MAX_H_REG = 8192;     // the widest row that 16 warps of 16 elements a thread hold (32 warps in the forward: 16384)
+constexpr int DEPTH = 3;            // stages of a ring: two in flight, one being read
+constexpr int MAX_H_REG = 8192;     // the widest row that 16 warps of two vectors a thread hold (with its shift)
 
 __device__ __forceinline__ void group_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -45,101 +56,222 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int W, int warp_in_gro
   warp_sums<N>(v);
 }
 
+// 16 bytes, or the first `bytes` of them and zeros, from global to shared memory.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* p, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
+
+// 1 / sqrt(v): the fast approximation (2 units in the last place) and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+}
+
+// A thread's NV vectors of a row whose first element is the shift-th of its granule: vector t + k T holds the
+// columns col[k] .. col[k] + 7, of which lo[k] .. hi[k] - 1 exist. EDGE = false: rows of whole granules (every
+// vector is full or absent), which spares the checks.
+template <int NV, bool EDGE>
+struct Cols {
+  int col[NV], lo[NV], hi[NV];
+  __device__ __forceinline__ Cols(int t, int T, int shift, int H) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      col[k] = 8 * (t + k * T) - shift;
+      lo[k] = max(0, -col[k]);
+      hi[k] = min(8, H - col[k]);
+      if (hi[k] <= lo[k]) lo[k] = hi[k] = 0;
+    }
+  }
+  __device__ __forceinline__ bool any(int k) const { return hi[k] > 0; }
+  __device__ __forceinline__ bool partial(int k) const { return EDGE ? hi[k] - lo[k] != 8 : false; }
+  // the vector with zeros outside the row (absent vectors read zeros from the ring already)
+  __device__ __forceinline__ void mask(int k, uint32_t (&w)[4]) const {
+    if (partial(k)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (2 * i < lo[k] || 2 * i >= hi[k]) w[i] &= 0xffff0000u;
+        if (2 * i + 1 < lo[k] || 2 * i + 1 >= hi[k]) w[i] &= 0x0000ffffu;
+      }
+    }
+  }
+  // Starts the copy of a vector of the row `row`, `at` elements into its operand. What lies in front of the row in
+  // its first granule comes along (it belongs to the row before); in front of the operand itself nothing is read.
+  __device__ __forceinline__ void fetch(int k, uint32_t dst, const __nv_bfloat16* row, int64_t at) const {
+    if (!any(k)) return;  // its place in the ring holds zeros from the start
+    if (!EDGE || at + col[k] >= 0) {
+      copy_async(dst, row + col[k], EDGE ? hi[k] * 2 : 16);
+    } else {
+      for (int i = lo[k]; i < hi[k]; ++i)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * i), "h"(reinterpret_cast<const uint16_t*>(row)[col[k] + i])
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void store(int k, __nv_bfloat16* row, const uint32_t (&w)[4]) const {
+    if (!any(k)) return;
+    if (!partial(k)) {
+      *reinterpret_cast<uint4*>(row + col[k]) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= lo[k] && i < hi[k])
+          reinterpret_cast<uint16_t*>(row)[col[k] + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+  }
+  // Zeros for the absent vectors of `slots` places of the ring, `pitch` bytes apart.
+  __device__ __forceinline__ void clear_absent(uint32_t ring, int T, int slots, uint32_t pitch) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (!any(k))
+        for (int i = 0; i < slots; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i * pitch + k * T * 16), "r"(0) : "memory");
+  }
+  // bf16 values of a vector over the columns (gain or bias), `fill` where there are none
+  __device__ __forceinline__ void gather(int k, const __nv_bfloat16* p, float fill, f2 (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = 2 * i, b = 2 * i + 1;
+      v[i] = f2_make(p && a >= lo[k] && a < hi[k] ? __bfloat162float(p[col[k] + a]) : fill,
+                     p && b >= lo[k] && b < hi[k] ? __bfloat162float(p[col[k] + b]) : fill);
+    }
+  }
+};
+
+// The group's place: rows first, first + stride, ... of one shift.
+__device__ __forceinline__ int row_shift(const void* base, int64_t ld, int64_t row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(base) / 2 + static_cast<uint64_t>(row) * static_cast<uint64_t>(ld)) & 7);
+}
+
 struct LnFwd {
   const __nv_bfloat16* x;
   const __nv_bfloat16 *g, *b;
   __nv_bfloat16* y;
   float *mean, *rstd;
-  int64_t ld_x, ld_y, rows;
+  int64_t ld_x, ld_y, rows, stride;  // stride: rows from one of a group's to its next; hop: elements, likewise
+  int64_t hop_x, hop_y;
   int H, W;
-  float eps;
+  float eps, inv_h;
 };
 
-// Groups of W warps, each a row at a time; the next row's loads are issued before this row's sums.
-template <int VEC, int EPT>
-__global__ void __launch_bounds__(1024, 1) layernorm_fwd_kernel(LnFwd a) {
-  using V = typename Raw<VEC>::type;
-  constexpr int NV = EPT / VEC;
-  __shared__ float red[2][32];
+// Two rows at a time: one exchange of two sums serves both.
+template <int NV, bool EDGE, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __grid_constant__ LnFwd a) {
+  constexpr int R = 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[2][32 * R];
   const int warp = threadIdx.x >> 5, W = a.W, T = W * 32;
   const int group = warp / W, wig = warp - group * W, groups = blockDim.x / T;
   const int t = threadIdx.x - group * T;
-  const int nvec = a.H / VEC;
-  const float inv_h = 1.0f / static_cast<float>(a.H);
-  V xv[NV], nx[NV];
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  auto load = [&](V(&d)[NV], int64_t r) {
-    const V* p = reinterpret_cast<const V*>(a.x + r * a.ld_x);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+  if (first >= a.rows) return;  // whole groups leave; nothing below waits for another group
+  const Cols<NV, EDGE> cols(t, T, row_shift(a.x, a.ld_x, first), a.H);
+  const uint32_t slice = static_cast<uint32_t>(T) * NV * 16;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + group * (DEPTH * R * slice) + t * 16;
+  const uint32_t ring_end = ring + DEPTH * R * slice;
+  f2 gain[NV][4], bias[NV][4];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (t + k * T < nvec)
-        d[k] = p[t + k * T];
-      else
-        zero(d[k]);
+  for (int k = 0; k < NV; ++k) {
+    cols.gather(k, a.g, 1.f, gain[k]);
+    cols.gather(k, a.b, 0.f, bias[k]);
+  }
+  cols.clear_absent(ring, T, DEPTH * R, slice);
+  int64_t next = first, x_at = first * a.ld_x;  // the row to fetch next and its place
+  const __nv_bfloat16* x_row = a.x + x_at;
+  auto fill = [&](uint32_t to) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (next < a.rows) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) cols.fetch(k, to + r * slice + k * T * 16, x_row, x_at);
+      }
+      next += a.stride;
+      x_row += a.hop_x;
+      x_at += a.hop_x;
     }
+    copy_commit();
   };
-  if (row < a.rows) load(xv, row);
-  for (; row < a.rows; row += step) {
-    const bool more = row + step < a.rows;
-    if (more) load(nx, row + step);
-    float f[EPT];
+  __nv_bfloat16* out = a.y + first * a.ld_y;
+  uint32_t to = ring, at = ring;
+  for (int s = 0; s < DEPTH - 1; ++s, to += R * slice) fill(to);
+  for (int64_t row0 = first; row0 < a.rows; row0 += R * a.stride) {
+    fill(to);
+    to += R * slice;
+    if (to == ring_end) to = ring;
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    f2 x[R][NV][4];
+    float s[R];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) unpack(xv[k], f + k * VEC);
-    float s[1] = {0.f};
+    for (int r = 0; r < R; ++r) {
+      f2 sum = 0;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) s[0] += f[i];
-    group_sums<1>(s, W, wig, 1 + group, red[0] + group * W);
-    const float mean = s[0] * inv_h;
-    float q[1] = {0.f};
+      for (int k = 0; k < NV; ++k) {
+        uint32_t w[4];
+        lds128(at + r * slice + k * T * 16, w);
+        cols.mask(k, w);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const bool in = t + k * T < nvec;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float c = f[k * VEC + i] - mean;
-        f[k * VEC + i] = c;
-        if (in) q[0] = fmaf(c, c, q[0]);
-      }
-    }
-    group_sums<1>(q, W, wig, 1 + group, red[1] + group * W);
-    const float rstd = 1.0f / sqrtf(q[0] * inv_h + a.eps);
-    if (t == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-    V* yp = reinterpret_cast<V*>(a.y + row * a.ld_y);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = t + k * T;
-      if (c < nvec) {
-        float o[VEC], w[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = f[k * VEC + i] * rstd;
-        if (a.g) {
-          unpack(__ldg(reinterpret_cast<const V*>(a.g) + c), w);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) o[i] *= w[i];
+        for (int i = 0; i < 4; ++i) {
+          x[r][k][i] = f2_of(w[i]);
+          sum = f2_add(sum, x[r][k][i]);
         }
-        if (a.b) {
-          unpack(__ldg(reinterpret_cast<const V*>(a.b) + c), w);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) o[i] += w[i];
-        }
-        V out;
-        pack(out, o);
-        yp[c] = out;
       }
+      s[r] = f2_sum(sum);
     }
-    if (more) {
+    at += R * slice;
+    if (at == ring_end) at = ring;
+    group_sums<R>(s, W, wig, 1 + group, red[0] + group * W * R);
+    float q[R], mean[R];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) xv[k] = nx[k];
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * a.inv_h;
+      const f2 neg = f2_both(-mean[r]);
+      f2 sum = 0;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[r][k][i] = f2_add(x[r][k][i], neg);
+        if (!EDGE && !cols.any(k)) continue;
+        if (cols.partial(k)) {  // what is outside the row adds nothing
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            f2_split(x[r][k][i], lo, hi);
+            x[r][k][i] = f2_make(2 * i >= cols.lo[k] && 2 * i < cols.hi[k] ? lo : 0.f,
+                                 2 * i + 1 >= cols.lo[k] && 2 * i + 1 < cols.hi[k] ? hi : 0.f);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = f2_fma(x[r][k][i], x[r][k][i], sum);
+      }
+      q[r] = f2_sum(sum);
+    }
+    group_sums<R>(q, W, wig, 1 + group, red[1] + group * W * R);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = row0 + r * a.stride;
+      if (row >= a.rows) continue;
+      const float rstd = inv_sqrt(fmaf(q[r], a.inv_h, a.eps));
+      if (t == 0) {
+        if (a.mean) a.mean[row] = mean[r];
+        if (a.rstd) a.rstd[row] = rstd;
+      }
+      const f2 rs = f2_both(rstd);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = f2_pack(f2_fma(f2_mul(x[r][k][i], rs), gain[k][i], bias[k][i]));
+        cols.store(k, out, w);
+      }
+      out += a.hop_y;
     }
   }
 }
 
-// Rows wider than the registers of a CTA hold: one CTA a row, three passes over it (the second and third
-// from L2), an element at a time.
+// Rows wider than the registers of a CTA hold, and operands whose rows lie differently in their granules: one
+// CTA a row, three passes over it (the second and third from L1 or L2), an element at a time.
 __global__ void __launch_bounds__(1024, 1) layernorm_fwd_wide_kernel(LnFwd a) {
   __shared__ float red[2][32];
   const int wig = threadIdx.x >> 5;
@@ -147,20 +279,20 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_wide_kernel(LnFwd a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const __nv_bfloat16* x = a.x + row * a.ld_x;
     float s[1] = {0.f}, q[1] = {0.f};
-    for (int j = threadIdx.x; j < a.H; j += 1024) s[0] += __bfloat162float(x[j]);
-    group_sums<1>(s, 32, wig, 1, red[0]);
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) s[0] += __bfloat162float(x[j]);
+    group_sums<1>(s, blockDim.x >> 5, wig, 1, red[0]);
     const float mean = s[0] * inv_h;
-    for (int j = threadIdx.x; j < a.H; j += 1024) {
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
       const float c = __bfloat162float(x[j]) - mean;
       q[0] = fmaf(c, c, q[0]);
     }
-    group_sums<1>(q, 32, wig, 1, red[1]);
+    group_sums<1>(q, blockDim.x >> 5, wig, 1, red[1]);
     const float rstd = 1.0f / sqrtf(q[0] * inv_h + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    for (int j = threadIdx.x; j < a.H; j += 1024) {
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
       float o = (__bfloat162float(x[j]) - mean) * rstd;
       if (a.g) o *= __bfloat162float(a.g[j]);
       if (a.b) o += __bfloat162float(a.b[j]);
@@ -178,191 +310,124 @@ struct LnBwd {
   __nv_bfloat16* dx;
   float* part;  // [gridDim.x][2][H]: partial dg and db; the final dg and db themselves with one CTA
   float *dg, *db;
-  int64_t ld_dy, ld_x, ld_dres, ld_dx, rows;
-  int H, W, depth;
+  int64_t ld_dy, ld_x, ld_dres, ld_dx, rows, stride;
+  int64_t hop_dy, hop_x, hop_dres, hop_dx;
+  int H, W;
+  float inv_h;
 };
 
-// 16 or 4 bytes from global to shared memory, zeros where `live` is false (p is then any valid address).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* p, bool live) {
-  const int n = live ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-}
-
-// Groups of W warps, R rows at a time (one exchange of 2R sums serves them). Rows arrive through a ring of
-// `depth` stages that cp.async fills, `depth` - 1 ahead; a thread copies exactly the vectors that it reads,
-// so the ring needs no barrier. Rows of single elements (VEC = 1: odd H or row stride), for which there is no
-// such copy, come through registers, and more CTAs to an SM hide their latency.
-template <int VEC, int EPT, int R>
-__global__ void __launch_bounds__(512, 1) layernorm_bwd_kernel(LnBwd a) {
-  using V = typename Raw<VEC>::type;
-  constexpr int NV = EPT / VEC;
-  constexpr bool RING = VEC > 1;
+// A row at a time, the next ones in flight.
+template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __grid_constant__ LnBwd a) {
+  constexpr int TENSORS = RES ? 3 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [2][H] sums after the rows
-  __shared__ float red[2][32 * 4];
+  __shared__ float red[2][32 * 2];
   const int warp = threadIdx.x >> 5, W = a.W, T = W * 32;
   const int group = warp / W, wig = warp - group * W, groups = blockDim.x / T;
   const int t = threadIdx.x - group * T;
-  const int nvec = a.H / VEC;
-  const float inv_h = 1.0f / static_cast<float>(a.H);
-  const bool has_res = a.dres != nullptr;
-  const int tensors = has_res ? 3 : 2;
-  const uint32_t slice = static_cast<uint32_t>(T) * EPT * 2;  // one row of one tensor
-  const uint32_t stage = slice * R * tensors;
-  uint8_t* ring = smem + static_cast<size_t>(group) * a.depth * stage;
-  const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const Cols<NV, EDGE> cols(t, T, row_shift(a.x, a.ld_x, first), a.H);
+  const uint32_t slice = static_cast<uint32_t>(T) * NV * 16;  // one row of one operand
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + group * (DEPTH * TENSORS * slice) + t * 16;
+  const uint32_t ring_end = ring + DEPTH * TENSORS * slice;
 
-  float dg[EPT], db[EPT];
-  V gain[NV];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  f2 dg[NV][4], db[NV][4], gain[NV][4];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    zero(gain[k]);
-    if (a.g && t + k * T < nvec) gain[k] = __ldg(reinterpret_cast<const V*>(a.g) + t + k * T);
+    cols.gather(k, a.g, 1.f, gain[k]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0;
   }
-#pragma unroll
-  for (int i = 0; i < EPT; ++i) dg[i] = db[i] = 0.f;
-
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * R;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * groups + group) * R;
-  auto fill = [&](int slot, int64_t row0) {
-    if constexpr (RING) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool row_live = row0 + r < a.rows;
-        const int64_t row = row_live ? row0 + r : 0;
-        uint32_t dst = ring_addr + slot * stage + r * tensors * slice + t * VEC * 2;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          const bool live = row_live && t + k * T < nvec;
-          const int c = live ? (t + k * T) * VEC : 0;
-          const uint32_t o = dst + k * T * VEC * 2;
-          copy_async<VEC * 2>(o, a.dy + row * a.ld_dy + c, live);
-          copy_async<VEC * 2>(o + slice, a.x + row * a.ld_x + c, live);
-          if (has_res) copy_async<VEC * 2>(o + 2 * slice, a.dres + row * a.ld_dres + c, live);
-        }
-      }
-    }
-  };
-  auto stats = [&](int64_t row0, float(&m)[R], float(&s)[R]) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool live = row0 + r < a.rows;
-      m[r] = live ? a.mean[row0 + r] : 0.f;
-      s[r] = live ? a.rstd[row0 + r] : 0.f;
-    }
-  };
-  if constexpr (RING) {
-    for (int s = 0; s < a.depth - 1; ++s) {
-      fill(s, first + s * step);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-  }
-  float mean[R], rstd[R], next_mean[R], next_rstd[R];
-  stats(first, next_mean, next_rstd);
-  int buf = 0, slot = 0;
-  for (int64_t row0 = first; row0 < a.rows; row0 += step) {
-    V vdy[R][NV], vx[R][NV], vr[R][NV];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      mean[r] = next_mean[r];
-      rstd[r] = next_rstd[r];
-    }
-    stats(row0 + step, next_mean, next_rstd);
-    if constexpr (RING) {
-      fill(slot == 0 ? a.depth - 1 : slot - 1, row0 + (a.depth - 1) * step);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (a.depth == 2)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else if (a.depth == 3)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-      else
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r;
+  cols.clear_absent(ring, T, DEPTH * TENSORS, slice);
+  // the row to fetch next and its place in each operand
+  int64_t next = first, dy_at = first * a.ld_dy, x_at = first * a.ld_x, res_at = first * a.ld_dres;
+  const __nv_bfloat16 *dy_row = a.dy + dy_at, *x_row = a.x + x_at, *res_row = a.dres + res_at;
+  auto fill = [&](uint32_t to) {
+    if (next < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if constexpr (RING) {
-          const uint8_t* p = ring + slot * stage + r * tensors * slice + (t + k * T) * VEC * 2;
-          vdy[r][k] = *reinterpret_cast<const V*>(p);
-          vx[r][k] = *reinterpret_cast<const V*>(p + slice);
-          if (has_res)
-            vr[r][k] = *reinterpret_cast<const V*>(p + 2 * slice);
-          else
-            zero(vr[r][k]);
-        } else {
-          const bool live = row < a.rows && t + k * T < nvec;
-          const int c = t + k * T;
-          zero(vdy[r][k]);
-          zero(vx[r][k]);
-          zero(vr[r][k]);
-          if (live) {
-            vdy[r][k] = reinterpret_cast<const V*>(a.dy + row * a.ld_dy)[c];
-            vx[r][k] = reinterpret_cast<const V*>(a.x + row * a.ld_x)[c];
-            if (has_res) vr[r][k] = reinterpret_cast<const V*>(a.dres + row * a.ld_dres)[c];
-          }
-        }
+        const uint32_t dst = to + k * T * 16;
+        cols.fetch(k, dst, dy_row, dy_at);
+        cols.fetch(k, dst + slice, x_row, x_at);
+        if (RES) cols.fetch(k, dst + 2 * slice, res_row, res_at);
       }
     }
-    if (RING && ++slot == a.depth) slot = 0;
-    float s[2 * R];
+    next += a.stride;
+    dy_row += a.hop_dy;
+    x_row += a.hop_x;
+    if (RES) res_row += a.hop_dres;
+    if (EDGE) {
+      dy_at += a.hop_dy;
+      x_at += a.hop_x;
+      if (RES) res_at += a.hop_dres;
+    }
+    copy_commit();
+  };
+  __nv_bfloat16* out = a.dx + first * a.ld_dx;
+  uint32_t to = ring;
+  for (int s = 0; s < DEPTH - 1; ++s, to += TENSORS * slice) fill(to);
+  float next_mean = 0.f, next_rstd = 0.f;
+  if (first < a.rows) {
+    next_mean = a.mean[first];
+    next_rstd = a.rstd[first];
+  }
+  uint32_t at = ring;
+  int buf = 0;
+  for (int64_t row = first; row < a.rows; row += a.stride) {
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + a.stride < a.rows) {
+      next_mean = a.mean[row + a.stride];
+      next_rstd = a.rstd[row + a.stride];
+    }
+    fill(to);
+    to += TENSORS * slice;
+    if (to == ring_end) to = ring;
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    f2 xh[NV][4], w[NV][4], s0 = 0, s1 = 0;
+    const f2 rs = f2_both(rstd), off = f2_both(-mean * rstd);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s[2 * r] = s[2 * r + 1] = 0.f;
+    for (int k = 0; k < NV; ++k) {
+      uint32_t d[4], x[4];
+      lds128(at + k * T * 16, d);
+      lds128(at + slice + k * T * 16, x);
+      cols.mask(k, d);  // columns outside the row hold dy = 0 and x = 0: they add nothing to any sum
+      cols.mask(k, x);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        // columns past H and rows past the last hold dy = 0: they add nothing to any sum
-        float d[VEC], x[VEC], g[VEC];
-        unpack(vdy[r][k], d);
-        unpack(vx[r][k], x);
-        unpack(gain[k], g);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float xh = (x[i] - mean[r]) * rstd[r];
-          const float w = a.g ? d[i] * g[i] : d[i];
-          s[2 * r] += w;
-          s[2 * r + 1] = fmaf(w, xh, s[2 * r + 1]);
-          dg[k * VEC + i] = fmaf(d[i], xh, dg[k * VEC + i]);
-          db[k * VEC + i] += d[i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const f2 dv = f2_of(d[i]);
+        xh[k][i] = f2_fma(f2_of(x[i]), rs, off);
+        w[k][i] = f2_mul(dv, gain[k][i]);
+        s0 = f2_add(s0, w[k][i]);
+        s1 = f2_fma(w[k][i], xh[k][i], s1);
+        dg[k][i] = f2_fma(dv, xh[k][i], dg[k][i]);
+        db[k][i] = f2_add(db[k][i], dv);
       }
     }
-    group_sums<2 * R>(s, W, wig, 1 + group, red[buf] + group * W * 2 * R);
+    float s[2] = {f2_sum(s0), f2_sum(s1)};
+    group_sums<2>(s, W, wig, 1 + group, red[buf] + group * W * 2);
     buf ^= 1;
+    // dx = rstd w - rstd c1 - xh (rstd c2) + dres
+    const f2 k1 = f2_both(-rstd * (s[0] * a.inv_h)), k2 = f2_both(-rstd * (s[1] * a.inv_h));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r;
-      if (row >= a.rows) continue;
-      const float c1 = s[2 * r] * inv_h, c2 = s[2 * r + 1] * inv_h;
-      V* po = reinterpret_cast<V*>(a.dx + row * a.ld_dx);
+    for (int k = 0; k < NV; ++k) {
+      uint32_t o[4], r[4];
+      if (RES) lds128(at + 2 * slice + k * T * 16, r);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (t + k * T < nvec) {
-          float d[VEC], x[VEC], g[VEC], o[VEC];
-          unpack(vdy[r][k], d);
-          unpack(vx[r][k], x);
-          unpack(vr[r][k], o);
-          unpack(gain[k], g);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float xh = (x[i] - mean[r]) * rstd[r];
-            const float w = a.g ? d[i] * g[i] : d[i];
-            o[i] = fmaf(rstd[r], w - c1 - xh * c2, o[i]);
-          }
-          V out;
-          pack(out, o);
-          po[t + k * T] = out;
-        }
+      for (int i = 0; i < 4; ++i) {
+        f2 v = f2_fma(w[k][i], rs, f2_fma(xh[k][i], k2, k1));
+        if (RES) v = f2_add(v, f2_of(r[i]));
+        o[i] = f2_pack(v);
       }
+      cols.store(k, out, o);
     }
+    out += a.hop_dx;
+    at += TENSORS * slice;
+    if (at == ring_end) at = ring;
   }
-  if constexpr (RING) asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // the groups' sums, added in group order
+  // the groups' sums, added in group order (groups of one CTA may hold other columns: the sums meet by column)
   float* sums = reinterpret_cast<float*>(smem);
   float* pg = gridDim.x == 1 ? a.dg : a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
   float* pb = gridDim.x == 1 ? a.db : pg + a.H;
@@ -371,22 +436,24 @@ __global__ void __launch_bounds__(512, 1) layernorm_bwd_kernel(LnBwd a) {
     if (group == gi) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int c = t + k * T;
-        if (c < nvec) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            float vg = dg[k * VEC + i], vb = db[k * VEC + i];
-            const int j = c * VEC + i;
+        for (int i = 0; i < 8; ++i) {
+          if (i >= cols.lo[k] && i < cols.hi[k]) {
+            float vg[2], vb[2];
+            f2_split(dg[k][i / 2], vg[0], vg[1]);
+            f2_split(db[k][i / 2], vb[0], vb[1]);
+            float sg = vg[i & 1], sb = vb[i & 1];
+            const int j = cols.col[k] + i;
             if (gi > 0) {
-              vg += sums[j];
-              vb += sums[a.H + j];
+              sg += sums[j];
+              sb += sums[a.H + j];
             }
             if (gi + 1 < groups) {
-              sums[j] = vg;
-              sums[a.H + j] = vb;
+              sums[j] = sg;
+              sums[a.H + j] = sb;
             } else {
-              if (pg) pg[j] = vg;
-              if (pb) pb[j] = vb;
+              if (pg) pg[j] = sg;
+              if (pb) pb[j] = sb;
             }
           }
         }
@@ -395,22 +462,25 @@ __global__ void __launch_bounds__(512, 1) layernorm_bwd_kernel(LnBwd a) {
   }
 }
 
-// dg and db from `parts` partial rows of 2H floats: 32 columns a block, 8 threads a column, each the sum of
-// every eighth row, added in order.
-__global__ void __launch_bounds__(256) layernorm_bwd_reduce_kernel(const float* __restrict__ part, int parts, int H,
-                                                                   float* __restrict__ dg, float* __restrict__ db) {
-  __shared__ float red[8][32];
+// dg and db from `parts` partial rows of 2H floats: 32 columns a block, 32 threads a column, each the sum of
+// every 32nd row, added in order. Launched ahead of the pass's end (its CTAs start as that one's leave).
+constexpr int REDUCE_Y = 32;
+__global__ void __launch_bounds__(32 * REDUCE_Y) layernorm_bwd_reduce_kernel(const float* __restrict__ part, int parts, int H,
+                                                                             float* __restrict__ dg, float* __restrict__ db) {
+  __shared__ float red[REDUCE_Y][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane, cols = 2 * static_cast<int64_t>(H);
   float v = 0.f;
   if (j < cols) {
-#pragma unroll 8
-    for (int p = y; p < parts; p += 8) v += part[p * cols + j];
+#pragma unroll 10
+    for (int p = y; p < parts; p += REDUCE_Y) v += part[p * cols + j];
   }
   red[y][lane] = v;
   __syncthreads();
   if (y == 0 && j < cols) {
-    for (int k = 1; k < 8; ++k) v += red[k][lane];
+#pragma unroll
+    for (int k = 1; k < REDUCE_Y; ++k) v += red[k][lane];
     if (j < H) {
       if (dg) dg[j] = v;
     } else if (db) {
@@ -419,8 +489,9 @@ __global__ void __launch_bounds__(256) layernorm_bwd_reduce_kernel(const float* 
   }
 }
 
-// Rows wider than the registers of a CTA hold: dx a row at a time (the second pass from L2), then the column
-// sums in a kernel of their own (before dx, which may overwrite dy).
+// Rows wider than the registers of a CTA hold, and operands whose rows lie differently in their granules: the
+// column sums in a kernel of their own (before dx, which may overwrite dy), then dx a row at a time, the second
+// pass from L1 or L2.
 __global__ void __launch_bounds__(1024, 1) layernorm_bwd_wide_dx_kernel(LnBwd a) {
   __shared__ float red[2][64];
   const int wig = threadIdx.x >> 5;
@@ -430,14 +501,14 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_wide_dx_kernel(LnBwd a)
     const __nv_bfloat16 *dy = a.dy + row * a.ld_dy, *x = a.x + row * a.ld_x;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s[2] = {0.f, 0.f};
-    for (int j = threadIdx.x; j < a.H; j += 1024) {
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
       const float w = __bfloat162float(dy[j]) * (a.g ? __bfloat162float(a.g[j]) : 1.f);
       s[0] += w;
       s[1] = fmaf(w, (__bfloat162float(x[j]) - mean) * rstd, s[1]);
     }
-    group_sums<2>(s, 32, wig, 1, red[buf]);
+    group_sums<2>(s, blockDim.x >> 5, wig, 1, red[buf]);
     buf ^= 1;
-    for (int j = threadIdx.x; j < a.H; j += 1024) {
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
       const float w = __bfloat162float(dy[j]) * (a.g ? __bfloat162float(a.g[j]) : 1.f);
       const float xh = (__bfloat162float(x[j]) - mean) * rstd;
       const float r = a.dres ? __bfloat162float(a.dres[row * a.ld_dres + j]) : 0.f;
@@ -459,87 +530,114 @@ __global__ void __launch_bounds__(256) layernorm_bwd_wide_cols_kernel(LnBwd a) {
   a.part[static_cast<int64_t>(blockIdx.y) * 2 * a.H + a.H + j] = db;
 }
 
-// The widest vector that divides H and keeps every row of every operand aligned.
-struct RowsAlign {
-  uintptr_t bits = 0;
-  void add(const void* p, int64_t ld) {
-    if (p) bits |= reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld) * 2;
+// Whether the rows of all operands lie alike in their 16-byte granules, and how often their place repeats.
+struct Granules {
+  uintptr_t base, ld;
+  bool alike = true;
+  Granules(const void* p, int64_t l) : base(reinterpret_cast<uintptr_t>(p) & 15), ld(static_cast<uintptr_t>(l) & 7) {}
+  void add(const void* p, int64_t l) {
+    if (p && ((reinterpret_cast<uintptr_t>(p) & 15) != base || (static_cast<uintptr_t>(l) & 7) != ld)) alike = false;
   }
-  int vec(int H) const {
-    if (H % 8 == 0 && (bits & 15) == 0) return 8;
-    if (H % 2 == 0 && (bits & 3) == 0) return 2;
-    return 1;
-  }
+  int period() const { return ld == 0 ? 1 : ld % 4 == 0 ? 2 : ld % 2 == 0 ? 4 : 8; }
+  bool shifted() const { return base != 0 || ld != 0; }
 };
 
-// Warps of a group that hold H elements at EPT a thread, and groups of a CTA.
+// A pass's groups: W warps of NV vectors a thread, `groups` to a CTA, `ctas` CTAs; rings of smem bytes in all.
 struct Shape {
-  int W, groups;
+  int nv, W, groups, threads, ctas;
+  int64_t smem;
 };
-Shape group_shape(int H, int ept) {
+
+// threads_sm: threads of an SM that the pass's registers allow; rows_stage, tensors: rows and operands of a stage.
+// Works on a whole B200's 148 SMs whatever the device, so that results do not depend on it.
+Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_sm, int rows_stage, int tensors) {
   Shape s;
-  s.W = (H + 32 * ept - 1) / (32 * ept);
-  s.groups = std::max(1, GROUP_THREADS / (32 * s.W));
+  const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
+  s.nv = vecs <= one_vec ? 1 : 2;
+  s.W = (vecs + 32 * s.nv - 1) / (32 * s.nv);
+  s.groups = std::max(1, 8 / s.W);
+  s.threads = s.groups * s.W * 32;
+  const int resident = std::max(1, threads_sm / s.threads);
+  const int64_t want = (rows + s.groups - 1) / s.groups;
+  int64_t ctas = std::min<int64_t>(want, static_cast<int64_t>(SMS) * resident);
+  // the groups' stride has to be a multiple of the period
+  while (ctas * s.groups % g.period()) ++ctas;
+  s.ctas = static_cast<int>(ctas);
+  s.smem = static_cast<int64_t>(s.threads) * s.nv * 16 * rows_stage * tensors * DEPTH;
   return s;
 }
 
-template <int VEC, int EPT>
-mt_status fwd_go(LnFwd a, cudaStream_t st) {
-  const Shape s = group_shape(a.H, EPT);
-  a.W = s.W;
-  const int threads = s.groups * s.W * 32;
-  const int resident = std::max(1, 2048 / (threads * 2));  // about half the SM's threads at the kernel's registers
-  const int64_t want = (a.rows + s.groups - 1) / s.groups;
-  const int64_t grid = std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * resident);
-  layernorm_fwd_kernel<VEC, EPT><<<static_cast<unsigned>(grid), threads, 0, st>>>(a);
+constexpr int FWD_THREADS_SM = 512, BWD_THREADS_SM = 512;
+
+// The backward's registers (128 a thread with two vectors) leave room for two CTAs of up to 256 threads, rows of up
+// to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps on the SM than two vectors
+// and 320 of 128 do (32768 x 5120: 214 us against 228). Fewer registers spill into an L1 that the rings leave
+// small: 330 us.
+Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
+  const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
+  return shape_of(rows, H, g, vecs > 512 && vecs <= 640 ? 640 : 32, BWD_THREADS_SM, 1, res ? 3 : 2);
+}
+
+template <int NV, bool EDGE, int THREADS, int CTAS>
+mt_status fwd_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
+  static SmemOptIn opt;
+  if (s.smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(layernorm_fwd_kernel<NV, EDGE, THREADS, CTAS>)));
+  layernorm_fwd_kernel<NV, EDGE, THREADS, CTAS><<<s.ctas, s.threads, s.smem, st>>>(a);
   return launch_check("layernorm_fwd_kernel");
 }
 
-template <int EPT>
-mt_status fwd_vec(const LnFwd& a, int vec, cudaStream_t st) {
-  return vec == 8 ? fwd_go<8, EPT>(a, st) : vec == 2 ? fwd_go<2, EPT>(a, st) : fwd_go<1, EPT>(a, st);
+template <bool EDGE>
+mt_status fwd_shape_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
+  if (s.nv == 1) return fwd_go<1, EDGE, 256, 2>(a, s, st);
+  return s.threads <= 256 ? fwd_go<2, EDGE, 256, 2>(a, s, st) : fwd_go<2, EDGE, 512, 1>(a, s, st);
 }
 
-// Elements a thread and rows a step of the backward: two rows of 8 up to 4096 columns, one of 16 above.
-int bwd_ept(int H) { return H <= 4096 ? 8 : 16; }
-int bwd_rows(int H) { return H <= 4096 ? 2 : 1; }
+// Threads of a CTA that walks a row an element at a time.
+int wide_threads(int H) { return std::min(1024, std::max(32, (H + 127) / 128 * 32)); }
 
-// CTAs of the backward, each of which leaves one partial row: as many threads to an SM as its registers allow.
+mt_status layernorm_fwd_launch(LnFwd a, cudaStream_t st) {
+  Granules g(a.x, a.ld_x);
+  g.add(a.y, a.ld_y);
+  if (!g.alike || a.H + (g.shifted() ? 7 : 0) > MAX_H_REG) {
+    const int64_t grid = std::min<int64_t>(a.rows, static_cast<int64_t>(num_sms()) * 2048 / wide_threads(a.H));
+    layernorm_fwd_wide_kernel<<<static_cast<unsigned>(grid), wide_threads(a.H), 0, st>>>(a);
+    return launch_check("layernorm_fwd_wide_kernel");
+  }
+  const Shape s = shape_of(a.rows, a.H, g, 32, FWD_THREADS_SM, 2, 1);
+  a.W = s.W;
+  a.stride = static_cast<int64_t>(s.ctas) * s.groups;
+  a.hop_x = a.stride * a.ld_x;
+  a.hop_y = a.stride * a.ld_y;
+  return g.shifted() || a.H % 8 ? fwd_shape_go<true>(a, s, st) : fwd_shape_go<false>(a, s, st);
+}
+
+// Partial rows at most: of the register pass (rows of any alignment), or of the column pass.
 int bwd_parts(int64_t rows, int H) {
-  if (H > MAX_H_REG) return static_cast<int>(std::min<int64_t>(2 * SMS, (rows + 63) / 64));
-  const Shape s = group_shape(H, bwd_ept(H));
-  const int resident = std::max(2, std::min(4, 1024 / (s.groups * s.W * 32)));
-  const int64_t step = bwd_rows(H) * s.groups;
-  return static_cast<int>(std::min<int64_t>(SMS * resident, (rows + step - 1) / step));
+  const int wide = static_cast<int>(std::min<int64_t>(2 * SMS, (rows + 63) / 64));
+  if (H > MAX_H_REG) return wide;
+  int parts = wide;
+  for (int ld = 0; ld < 2; ++ld) parts = std::max(parts, bwd_shape(rows, H, Granules(nullptr, ld), false).ctas);
+  return parts;
 }
 
 uint64_t bwd_ws_bytes(int64_t rows, int H) {
   return static_cast<uint64_t>(align_up(static_cast<int64_t>(std::max(1, bwd_parts(rows, H))) * 2 * H * 4, 256));
 }
 
-template <int VEC, int EPT, int R>
-mt_status bwd_go(LnBwd a, int parts, cudaStream_t st) {
-  const Shape s = group_shape(a.H, EPT);
-  const int threads = s.groups * s.W * 32;
-  a.W = s.W;
-  a.depth = 0;
-  int64_t smem = s.groups > 1 ? 2ll * a.H * 4 : 0;  // groups > 1: H <= 1024
-  if (VEC > 1) {
-    // the deepest ring of 4 stages at most that leaves room for the other CTAs of the SM
-    const int64_t stage = static_cast<int64_t>(threads) * EPT * 2 * R * (a.dres ? 3 : 2);
-    const int64_t budget = 200 * 1024 / std::max(2, std::min(4, 1024 / threads));
-    a.depth = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(4, budget / stage)));
-    smem = std::max(smem, stage * a.depth);
-  }
+template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
+mt_status bwd_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
   static SmemOptIn opt;
-  if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(layernorm_bwd_kernel<VEC, EPT, R>)));
-  layernorm_bwd_kernel<VEC, EPT, R><<<parts, threads, smem, st>>>(a);
+  auto* kernel = layernorm_bwd_kernel<NV, EDGE, RES, THREADS, CTAS>;
+  const int64_t smem = std::max<int64_t>(s.smem, s.groups > 1 ? 2ll * a.H * 4 : 0);
+  if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(kernel)));
+  kernel<<<s.ctas, s.threads, smem, st>>>(a);
   return launch_check("layernorm_bwd_kernel");
 }
 
-template <int EPT, int R>
-mt_status bwd_vec(const LnBwd& a, int vec, int parts, cudaStream_t st) {
-  return vec == 8 ? bwd_go<8, EPT, R>(a, parts, st) : vec == 2 ? bwd_go<2, EPT, R>(a, parts, st) : bwd_go<1, EPT, R>(a, parts, st);
+template <bool EDGE, bool RES>
+mt_status bwd_shape_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
+  if (s.nv == 1) return s.threads <= 320 ? bwd_go<1, EDGE, RES, 320, 2>(a, s, st) : bwd_go<1, EDGE, RES, 640, 1>(a, s, st);
+  return s.threads <= 256 ? bwd_go<2, EDGE, RES, 256, 2>(a, s, st) : bwd_go<2, EDGE, RES, 512, 1>(a, s, st);
 }
 
 mt_status layernorm_bwd_launch(LnBwd a, cudaStream_t st) {
@@ -548,30 +646,46 @@ mt_status layernorm_bwd_launch(LnBwd a, cudaStream_t st) {
     if (a.db) MT_CUDA(cudaMemsetAsync(a.db, 0, static_cast<size_t>(a.H) * 4, st));
     return MT_OK;
   }
-  const int parts = bwd_parts(a.rows, a.H);
-  if (a.H > MAX_H_REG) {
+  Granules g(a.x, a.ld_x);
+  g.add(a.dy, a.ld_dy);
+  g.add(a.dres, a.ld_dres);
+  g.add(a.dx, a.ld_dx);
+  int parts;
+  if (!g.alike || a.H + (g.shifted() ? 7 : 0) > MAX_H_REG) {
+    parts = static_cast<int>(std::min<int64_t>(2 * SMS, (a.rows + 63) / 64));
     if (a.dg || a.db) {
       layernorm_bwd_wide_cols_kernel<<<dim3((a.H + 255) / 256, parts), 256, 0, st>>>(a);
       MT_TRY(launch_check("layernorm_bwd_wide_cols_kernel"));
     }
-    layernorm_bwd_wide_dx_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.rows, 2 * num_sms())), 1024, 0, st>>>(a);
+    const int64_t grid = std::min<int64_t>(a.rows, static_cast<int64_t>(num_sms()) * 2048 / wide_threads(a.H));
+    layernorm_bwd_wide_dx_kernel<<<static_cast<unsigned>(grid), wide_threads(a.H), 0, st>>>(a);
     MT_TRY(launch_check("layernorm_bwd_wide_dx_kernel"));
   } else {
-    RowsAlign al;
-    al.add(a.dy, a.ld_dy);
-    al.add(a.x, a.ld_x);
-    al.add(a.dres, a.ld_dres);
-    al.add(a.dx, a.ld_dx);
-    al.add(a.g, 0);
-    const int v = al.vec(a.H);
-    if (a.H <= 4096)
-      MT_TRY((bwd_vec<8, 2>(a, v, parts, st)));
+    const Shape s = bwd_shape(a.rows, a.H, g, a.dres != nullptr);
+    a.W = s.W;
+    a.stride = static_cast<int64_t>(s.ctas) * s.groups;
+    a.hop_dy = a.stride * a.ld_dy;
+    a.hop_x = a.stride * a.ld_x;
+    a.hop_dres = a.stride * a.ld_dres;
+    a.hop_dx = a.stride * a.ld_dx;
+    parts = s.ctas;
+    if (g.shifted() || a.H % 8)
+      MT_TRY((a.dres ? bwd_shape_go<true, true>(a, s, st) : bwd_shape_go<true, false>(a, s, st)));
     else
-      MT_TRY((bwd_vec<16, 1>(a, v, parts, st)));
+      MT_TRY((a.dres ? bwd_shape_go<false, true>(a, s, st) : bwd_shape_go<false, false>(a, s, st)));
     if (parts == 1) return MT_OK;
   }
   if (!a.dg && !a.db) return MT_OK;
-  layernorm_bwd_reduce_kernel<<<(2 * a.H + 31) / 32, 256, 0, st>>>(a.part, parts, a.H, a.dg, a.db);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((2 * a.H + 31) / 32, 1, 1);
+  cfg.blockDim = dim3(32 * REDUCE_Y, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MT_CUDA(cudaLaunchKernelEx(&cfg, layernorm_bwd_reduce_kernel, static_cast<const float*>(a.part), parts, a.H, a.dg, a.db));
   return launch_check("layernorm_bwd_reduce_kernel");
 }
 
@@ -608,18 +722,9 @@ mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, con
   a.H = H;
   a.W = 0;
   a.eps = eps;
-  if (H > 2 * MAX_H_REG) {
-    layernorm_fwd_wide_kernel<<<static_cast<unsigned>(std::min<int64_t>(rows, 2 * num_sms())), 1024, 0,
-                                as_stream(stream)>>>(a);
-    return launch_check("layernorm_fwd_wide_kernel");
-  }
-  RowsAlign al;
-  al.add(x, ld_x);
-  al.add(y, ld_y);
-  al.add(g, 0);
-  al.add(b, 0);
-  const int v = al.vec(H);
-  return H <= 256 ? fwd_vec<8>(a, v, as_stream(stream)) : fwd_vec<16>(a, v, as_stream(stream));
+  a.stride = 0;
+  a.inv_h = 1.0f / static_cast<float>(H);
+  return layernorm_fwd_launch(a, as_stream(stream));
 }
 
 uint64_t mt_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H) {
@@ -659,7 +764,9 @@ mt_status mt_layernorm_bwd(const mt_bf16* dy, int64_t ld_dy, const mt_bf16* x, i
   a.ld_dx = ld_dx;
   a.rows = rows;
   a.H = H;
-  a.W = a.depth = 0;
+  a.W = 0;
+  a.stride = 0;
+  a.inv_h = 1.0f / static_cast<float>(H);
   return layernorm_bwd_launch(a, as_stream(stream));
 }
 

@@ -24,6 +24,7 @@ using namespace vec;
 constexpr int MAX_PAIRS = 128, MAX_AXES = 8;
 constexpr int THREADS = 256;
 constexpr int TABLE = 2048;  // (cos, sin) pairs of a tile: 16 KiB
+constexpr int HG = 4;        // heads that share a thread's reads of the table
 
 struct Mrope {
   const __nv_bfloat16* x;
@@ -36,13 +37,33 @@ struct Mrope {
   double turns[MAX_PAIRS];
 };
 
+// Turns the pair (lo, hi) of VEC features by their (cos, sin).
+template <int VEC>
+__device__ __forceinline__ void turn(typename Raw<VEC>::type& lo, typename Raw<VEC>::type& hi, const float (&c)[VEC],
+                                     const float (&s)[VEC]) {
+  float l[VEC], h[VEC];
+  unpack(lo, l);
+  unpack(hi, h);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const float p = l[i], q = h[i];
+    l[i] = p * c[i] - q * s[i];
+    h[i] = q * c[i] + p * s[i];
+  }
+  pack(lo, l);
+  pack(hi, h);
+}
+
+// A thread takes one vector of features of HG heads of a token: their loads are in flight together, and the
+// feature's cos and sin are read from the table once for all of them.
 template <int VEC>
 __global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ Mrope a) {
   using V = typename Raw<VEC>::type;
-  __shared__ float2 table[TABLE];
-  const int rot = a.pairs / VEC;                                       // rotated vectors of a head half
-  const int tail = a.x == a.y ? 0 : (a.d - 2 * a.pairs) / VEC;         // vectors to copy behind them
-  const int per_head = rot + tail, per_token = per_head * a.heads;
+  // cos and sin, [token][feature within a vector][vector]: threads of neighbouring vectors read neighbouring words
+  __shared__ float cos_tab[TABLE], sin_tab[TABLE];
+  const int rot = a.pairs / VEC;                                // rotated vectors of a head half
+  const int tail = a.x == a.y ? 0 : (a.d - 2 * a.pairs) / VEC;  // vectors to copy behind them
+  const int head_groups = (a.heads + HG - 1) / HG;
   const int64_t tiles = (a.rows + a.tile - 1) / a.tile;
   for (int64_t tl = blockIdx.x; tl < tiles; tl += gridDim.x) {
     const int64_t row0 = tl * a.tile;
@@ -53,37 +74,49 @@ __global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ 
       const double p = static_cast<double>(a.pos[a.axis[i] * a.ld_pos + row0 + tok]) * a.turns[i];
       float s, c;
       sincospif(2.0f * static_cast<float>(p - rint(p)), &s, &c);
-      table[e] = make_float2(c, a.sign * s);
+      const int at = tok * a.pairs + (i % VEC) * rot + i / VEC;
+      cos_tab[at] = c;
+      sin_tab[at] = a.sign * s;
     }
     __syncthreads();
-    const int64_t items = static_cast<int64_t>(tokens) * per_token;
-    for (int64_t it = threadIdx.x; it < items; it += THREADS) {
-      const int tok = static_cast<int>(it / per_token), in_token = static_cast<int>(it - static_cast<int64_t>(tok) * per_token);
-      const int head = in_token / per_head, v = in_token - head * per_head;
-      const int64_t at = static_cast<int64_t>(head) * a.d;
-      const __nv_bfloat16* xh = a.x + (row0 + tok) * a.ld_x + at;
-      __nv_bfloat16* yh = a.y + (row0 + tok) * a.ld_y + at;
-      if (v < rot) {
-        const V lo = *reinterpret_cast<const V*>(xh + v * VEC), hi = *reinterpret_cast<const V*>(xh + a.pairs + v * VEC);
-        float l[VEC], h[VEC];
-        unpack(lo, l);
-        unpack(hi, h);
-        const float2* cs = table + tok * a.pairs + v * VEC;
+    const uint32_t per_token = rot * head_groups, items = tokens * per_token;
+    for (uint32_t it = threadIdx.x; it < items; it += THREADS) {
+      const uint32_t tok = it / per_token, in_token = it - tok * per_token;
+      const uint32_t hg = in_token / rot, v = in_token - hg * rot;
+      const int64_t at = static_cast<int64_t>(hg) * HG * a.d + v * VEC;
+      const __nv_bfloat16* x = a.x + (row0 + tok) * a.ld_x + at;
+      __nv_bfloat16* y = a.y + (row0 + tok) * a.ld_y + at;
+      const int n = min(HG, a.heads - static_cast<int>(hg) * HG);
+      V lo[HG], hi[HG];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float2 w = cs[i];
-          const float p = l[i], q = h[i];
-          l[i] = p * w.x - q * w.y;
-          h[i] = q * w.x + p * w.y;
+      for (int h = 0; h < HG; ++h) {
+        if (h < n) {
+          lo[h] = *reinterpret_cast<const V*>(x + h * a.d);
+          hi[h] = *reinterpret_cast<const V*>(x + h * a.d + a.pairs);
         }
-        V ol, oh;
-        pack(ol, l);
-        pack(oh, h);
-        *reinterpret_cast<V*>(yh + v * VEC) = ol;
-        *reinterpret_cast<V*>(yh + a.pairs + v * VEC) = oh;
-      } else {
-        const int c = 2 * a.pairs + (v - rot) * VEC;
-        *reinterpret_cast<V*>(yh + c) = *reinterpret_cast<const V*>(xh + c);
+      }
+      float c[VEC], s[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        c[i] = cos_tab[tok * a.pairs + i * rot + v];
+        s[i] = sin_tab[tok * a.pairs + i * rot + v];
+      }
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        if (h < n) {
+          turn<VEC>(lo[h], hi[h], c, s);
+          *reinterpret_cast<V*>(y + h * a.d) = lo[h];
+          *reinterpret_cast<V*>(y + h * a.d + a.pairs) = hi[h];
+        }
+      }
+    }
+    if (tail > 0) {
+      const int64_t copies = static_cast<int64_t>(tokens) * a.heads * tail;
+      for (int64_t it = threadIdx.x; it < copies; it += THREADS) {
+        const int64_t th = it / tail, tok = th / a.heads;
+        const int64_t at = (th - tok * a.heads) * a.d + 2 * a.pairs + (it - th * tail) * VEC;
+        *reinterpret_cast<V*>(a.y + (row0 + tok) * a.ld_y + at) =
+            *reinterpret_cast<const V*>(a.x + (row0 + tok) * a.ld_x + at);
       }
     }
   }
@@ -91,9 +124,9 @@ __global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ 
 
 template <int VEC>
 mt_status go(Mrope a, cudaStream_t st) {
-  const int64_t per_token = static_cast<int64_t>(a.heads) * ((a.x == a.y ? 0 : a.d - 2 * a.pairs) + a.pairs) / VEC;
-  // tokens of a tile: at least a thread's worth of vectors, no more than the table holds, and no more than
-  // leaves every SM a few tiles
+  const int64_t per_token = static_cast<int64_t>((a.heads + HG - 1) / HG) * (a.pairs / VEC);
+  // tokens of a tile: at least a vector for each thread, no more than the table holds, and no more than leaves
+  // every SM eight tiles
   const int64_t sms = num_sms();
   int64_t tile = std::max<int64_t>((THREADS + per_token - 1) / per_token, a.rows / (sms * 8));
   tile = std::max<int64_t>(1, std::min<int64_t>(tile, TABLE / a.pairs));
@@ -125,7 +158,7 @@ extern "C" mt_status mt_mrope(const mt_bf16* x, int64_t ld_x, mt_bf16* y, int64_
                 head_dim / 2);
   if (pairs > MAX_PAIRS) return fail(MT_ERR_UNSUPPORTED, "mrope: at most %d rotated pairs a head", MAX_PAIRS);
   const int64_t width = static_cast<int64_t>(n_heads) * head_dim;
-  if (width >= (1ll << 31)) return fail(MT_ERR_UNSUPPORTED, "mrope: heads of 2^31 columns and more");
+  if (width >= (1ll << 27)) return fail(MT_ERR_UNSUPPORTED, "mrope: heads of 2^27 columns and more");
   if (ld_x < width || ld_y < width || ld_pos < rows) return fail(MT_ERR_INVALID_ARG, "mrope: ld too small");
   if (x && x == y && ld_x != ld_y) return fail(MT_ERR_INVALID_ARG, "mrope: in place needs ld_x == ld_y");
   const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y);

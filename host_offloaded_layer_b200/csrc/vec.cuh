@@ -70,6 +70,50 @@ __device__ __forceinline__ void zero(uint4& u) { u = make_uint4(0u, 0u, 0u, 0u);
 __device__ __forceinline__ void zero(uint32_t& u) { u = 0u; }
 __device__ __forceinline__ void zero(uint16_t& u) { u = 0; }
 
+// Two fp32 values in a register pair: sm_100's packed arithmetic does both in one instruction.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 f2_both(float v) { return f2_make(v, v); }
+__device__ __forceinline__ void f2_split(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  float a, b;
+  f2_split(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_of(uint32_t w) { return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t f2_pack(f2 v) {
+  float a, b;
+  f2_split(v, a, b);
+  return pack2(a, b);
+}
+__device__ __forceinline__ void words(const uint4& u, uint32_t (&w)[4]) {
+  w[0] = u.x;
+  w[1] = u.y;
+  w[2] = u.z;
+  w[3] = u.w;
+}
+
 // Sums of N values (N = 1, 2 or 4) over the warp, left in every lane. The first log2(N) exchanges halve the
 // number of values a lane carries, so N = 4 takes 10 shuffles instead of 20; the order of additions is fixed.
 template <int N>

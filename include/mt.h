@@ -208,11 +208,12 @@ mt_status mt_rmsnorm_bwd_noalloc(const mt_bf16* dy, const mt_bf16* x, const mt_b
 /* LayerNorm forward over rows of H (any H >= 1): mean = sum x / H, rstd =
  * 1/sqrt(sum (x - mean)^2 / H + eps), y = (x - mean) * rstd * g + b. x and y are
  * [rows] of H elements, ld_x and ld_y elements apart; what lies between H and
- * the row stride is neither read nor written. g, b (bf16 [H]) and mean, rstd
- * (fp32 [rows] out, what the backward needs) may each be NULL. y may be x (same
- * row stride); they must not overlap otherwise. Pointers need the alignment of
- * their elements only; 16-byte aligned rows (pointers and strides of 8
- * elements, H a multiple of 8) are faster. H above 2^28: MT_ERR_UNSUPPORTED. */
+ * the row stride is not written, and no value of it is used. g, b (bf16 [H]) and
+ * mean, rstd (fp32 [rows] out, what the backward needs) may each be NULL. y may
+ * be x (same row stride); they must not overlap otherwise. Pointers need the
+ * alignment of their elements only; operands whose rows lie alike in their
+ * 16-byte granules (same address and stride modulo 16 bytes) are faster. H above
+ * 2^28: MT_ERR_UNSUPPORTED. */
 mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, const mt_bf16* b, mt_bf16* y,
                            int64_t ld_y, float* mean, float* rstd, int64_t rows, int32_t H, float eps, void* stream);
 
