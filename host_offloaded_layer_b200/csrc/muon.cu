@@ -71,10 +71,10 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-// The passes over the matrix walk tiles of (256 / tx) * 8 rows and tx * VEC columns, tx a power of two that
-// fits narrow matrices, VEC = 4 where rows are 16-byte aligned.
+// The passes over the matrix walk tiles of (256 / tx) * reps rows and tx * VEC columns, tx a power of two that
+// fits narrow matrices, VEC = 4 where rows are 16-byte aligned, reps up to 8 (fewer in small matrices).
 struct Walk {
-  int tx_log2;
+  int tx_log2, reps;
   int64_t col_tiles, tiles;
 };
 
@@ -87,8 +87,8 @@ __device__ __forceinline__ void walk(const Walk& w, int64_t rows, int64_t cols, 
     const int64_t col = (ct * tx + x) * VEC;
     if (col >= cols) continue;
 #pragma unroll 4
-    for (int k = 0; k < 8; ++k) {
-      const int64_t row = rt * (8 * ty) + k * ty + y;
+    for (int k = 0; k < w.reps; ++k) {
+      const int64_t row = rt * (w.reps * ty) + k * ty + y;
       if (row < rows) f(row, col);
     }
   }
@@ -110,9 +110,36 @@ __device__ __forceinline__ void ldv(float (&d)[VEC], const float* p) {
   *reinterpret_cast<typename F32<VEC>::type*>(d) = *reinterpret_cast<const typename F32<VEC>::type*>(p);
 }
 
+// The kernels of an update are launched one ahead: each starts when the one before it has started everywhere, sets
+// itself up, and waits here until that one has completed before it touches what it works on.
+__device__ __forceinline__ void release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... Params, class... Args>
+mt_status launch_ahead(void (*kernel)(Params...), const char* name, int grid, int threads, int64_t smem, int cluster,
+                       cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  MT_CUDA(cudaLaunchKernelEx(&cfg, kernel, Params(args)...));
+  return launch_check(name);
+}
+
 // Writes m' and a partial |u|^2 (fp64) a CTA.
 template <int VEC>
 __global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* __restrict__ parts) {
+  release_next();
   double s = 0.0;
   walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
     float g[VEC], m[VEC];
@@ -140,6 +167,8 @@ template <int VEC>
 __global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* __restrict__ parts, int n_parts,
                                                          double eps, __half* __restrict__ hi, __half* __restrict__ lo,
                                                          int64_t ld_x) {
+  release_next();
+  wait_for_last();
   double s = 0.0;
   for (int i = threadIdx.x; i < n_parts; i += 256) s += parts[i];
   s = block_sum(s);
@@ -207,30 +236,28 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The addend of 16 columns of a row (zeros where there is none): issued before the products are waited for.
+struct Addend {
+  uint32_t hi[8], lo[8];
+};
+__device__ __forceinline__ void load_addend(const NsArgs& e, int row, int col0, Addend& a) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a.hi[i] = a.lo[i] = 0u;
+  if (e.add_hi && row < e.M && col0 < e.N) {
+    const int64_t at = static_cast<int64_t>(row) * e.ld_add + col0;
+    ld32B(e.add_hi + at, a.hi);
+    if (e.add_lo) ld32B(e.add_lo + at, a.lo);
+  }
+}
+
 // Epilogue of 16 columns of the 32 rows that a warp holds, one row a lane (all lanes call it).
-__device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, float (&v)[16], bool mirror) {
+__device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, float (&v)[16], const Addend& a, bool mirror) {
   const bool live = row < e.M;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] *= e.alpha;
-  if (e.add_hi && live) {
-    uint32_t w[8];
-    const int64_t at = static_cast<int64_t>(row) * e.ld_add + col0;
-    ld32B(e.add_hi + at, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = h2f(w[i]);
-      v[2 * i] = fmaf(e.beta, f.x, v[2 * i]);
-      v[2 * i + 1] = fmaf(e.beta, f.y, v[2 * i + 1]);
-    }
-    if (e.add_lo) {
-      ld32B(e.add_lo + at, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = h2f(w[i]);
-        v[2 * i] = fmaf(e.beta, f.x, v[2 * i]);
-        v[2 * i + 1] = fmaf(e.beta, f.y, v[2 * i + 1]);
-      }
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float2 h = h2f(a.hi[i]), l = h2f(a.lo[i]);
+    v[2 * i] = fmaf(e.beta, l.x, fmaf(e.beta, h.x, v[2 * i] * e.alpha));
+    v[2 * i + 1] = fmaf(e.beta, l.y, fmaf(e.beta, h.y, v[2 * i + 1] * e.alpha));
   }
   if (e.diag != 0.f) {
 #pragma unroll
@@ -373,7 +400,7 @@ __device__ __forceinline__ uint64_t step_desc(uint32_t base, int kk) {
 // next tile runs.
 template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
-    ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, NsArgs ep,
+    ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsArgs ep,
                    int32_t* err) {
   constexpr int KA = 2, STAGES = ATOMS / KA, OP_STAGE = HALF * KA, BK = 64 * KA;
   extern __shared__ uint8_t smem_raw[];
@@ -394,6 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const int num_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
   const int num_kb = (ep.K + BK - 1) / BK;
 
+  release_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -415,6 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  wait_for_last();
 
   if (warp == 0) {
     uint32_t it = 0;
@@ -514,6 +543,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       for (int c = 0; c < 8; ++c) {
         const int col0 = nb * 256 + c * 32;
         if (col0 >= ep.N) break;
+        Addend add[2];
+        load_addend(ep, row, col0, add[0]);
+        load_addend(ep, row, col0 + 16, add[1]);
         uint32_t r[32];
         tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
 #pragma unroll
@@ -522,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
-          finish16(ep, row, col0 + 16 * h, v, ep.sym && mb != nb);
+          finish16(ep, row, col0 + 16 * h, v, add[h], ep.sym && mb != nb);
         }
       }
       fence_before();
@@ -542,15 +574,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- 128 x 128 tiles on one SM, K split over a cluster
-// For matrices with too few 256 x 256 tiles to fill the GPU: one tile a cluster of 1 to 8 CTAs, each of which
-// sums its share of K in its own TMEM. With more than one, the shares meet in shared memory: every CTA leaves its
-// fp32 tile there and each finishes 128 / size columns, adding the peers' tiles in rank order.
+// For matrices with too few 256 x 256 tiles to fill the GPU, where a product takes microseconds and latencies are
+// what counts: one tile a cluster of 1 to 8 CTAs, each of which sums its share of K in its own TMEM. With more than
+// one, the shares meet in shared memory: every CTA leaves its fp32 tile there and each finishes 128 / size columns,
+// adding the peers' tiles in rank order. Eight epilogue warps, two to a TMEM lane quarter, fetch the addend while
+// the products run.
 constexpr int RED_LD = 132;  // floats of a row of the shared tile: 16-byte accesses of 8 rows hit 32 banks
 static_assert(128 * RED_LD * 4 <= RING, "the tile overlays the ring");
+constexpr int TILE_THREADS = 64 + 256;
 
 template <bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(NS_THREADS, 1)
-    ns_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, NsArgs ep,
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    ns_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsArgs ep,
                    int32_t* err) {
   constexpr int STAGES = ATOMS;
   extern __shared__ uint8_t smem_raw[];
@@ -572,6 +607,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * rank / size);
   const int kb1 = static_cast<int>(static_cast<int64_t>(atoms) * (rank + 1) / size);  // size <= atoms: never empty
 
+  release_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -580,6 +616,8 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     mbar_init(smem_u32(tfull), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -589,7 +627,16 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  wait_for_last();
 
+  // What an epilogue thread finishes: `count` groups of 16 columns from first_col of row in_tile (its lane quarter's
+  // row; the two warps of a quarter take the columns by halves).
+  const int in_tile = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
+  const int share16 = 8 / size, count = share16 >= 2 ? share16 / 2 : (half == 0 ? share16 : 0);
+  const int first_col = nb * 128 + rank * (128 / size) + half * count * 16;
+  const int row = mb * 128 + in_tile;
+  const bool mirror = ep.sym && mb != nb;
+  Addend add[4];
   bool done = true;  // this warp's waits all ended
   if (warp == 0) {
     const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
@@ -629,27 +676,29 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     if (ok && lane == 0) umma_commit(smem_u32(tfull));
     __syncwarp();
   } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < count) load_addend(ep, row, first_col + 16 * c, add[c]);
     done = warp_wait(smem_u32(tfull), 0, abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
     fence_after();
-    const int q = warp & 3, in_tile = q * 32 + lane;
-    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     if (done) {
-      for (int c = 0; c < 4; ++c) {
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t r[32];
         tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
         if (size == 1) {
-          const int col0 = nb * 128 + c * 32;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (col0 + 16 * h >= ep.N) break;
+            const int col0 = first_col + c * 32 + 16 * h;
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
-            finish16(ep, mb * 128 + in_tile, col0 + 16 * h, v, ep.sym && mb != nb);
+            if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror);
           }
         } else {
           // every product that read the ring has completed: the tile may overlay it
-          float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + in_tile * RED_LD + c * 32);
+          float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + in_tile * RED_LD + half * 64 + c * 32);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             p[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
@@ -663,30 +712,38 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   if (size > 1) {
     cluster_sync();
     if (warp >= 2 && done) {
-      const int in_tile = (warp & 3) * 32 + lane, share = 128 / size;
-      for (int c = 0; c < share; c += 16) {
-        const int in_col = rank * share + c, col0 = nb * 128 + in_col;
-        if (col0 >= ep.N) break;
-        float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        const uint32_t at = smem_u32(smem) + (in_tile * RED_LD + in_col) * 4;
-        for (int p = 0; p < size; ++p) {
-          const uint32_t from = map_to_rank(at, static_cast<uint32_t>(p));
+      for (int c = 0; c < 2; ++c) {
+        const int col0 = first_col + 16 * c;
+        if (c < count && col0 < ep.N) {
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 f;
-            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                         : "r"(from + 16 * i)
-                         : "memory");
-            v[4 * i] += f.x;
-            v[4 * i + 1] += f.y;
-            v[4 * i + 2] += f.z;
-            v[4 * i + 3] += f.w;
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          const uint32_t at = smem_u32(smem) + (in_tile * RED_LD + (col0 - nb * 128)) * 4;
+          for (int p = 0; p < size; p += 2) {  // two peers' reads in flight
+            float4 f[2][4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t from = map_to_rank(at, static_cast<uint32_t>(p + q));
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(f[q][i].x), "=f"(f[q][i].y), "=f"(f[q][i].z), "=f"(f[q][i].w)
+                             : "r"(from + 16 * i)
+                             : "memory");
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[4 * i] += f[q][i].x;
+                v[4 * i + 1] += f[q][i].y;
+                v[4 * i + 2] += f[q][i].z;
+                v[4 * i + 3] += f[q][i].w;
+              }
           }
+          finish16(ep, row, col0, v, add[c], mirror);
         }
-        finish16(ep, mb * 128 + in_tile, col0, v, ep.sym && mb != nb);
       }
     }
     cluster_sync();  // no CTA leaves while a peer reads its tile
@@ -718,25 +775,12 @@ mt_status ns_launch(const CUtensorMap& ta, const CUtensorMap& tb, const NsArgs& 
     static SmemOptIn opt;
     MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_pair_kernel<A_MN, B_MN>)));
     const int clusters = std::min(ns_tiles(e, 256), pair_clusters());
-    ns_pair_kernel<A_MN, B_MN><<<2 * clusters, NS_THREADS, SMEM_BYTES, st>>>(ta, tb, e, err);
-    return launch_check("ns_pair_kernel");
+    return launch_ahead(ns_pair_kernel<A_MN, B_MN>, "ns_pair_kernel", 2 * clusters, NS_THREADS, SMEM_BYTES, 0, st, ta, tb, e, err);
   }
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_tile_kernel<A_MN, B_MN>)));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ns_tiles(e, 128) * split, 1, 1);
-  cfg.blockDim = dim3(NS_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  MT_CUDA(cudaLaunchKernelEx(&cfg, ns_tile_kernel<A_MN, B_MN>, ta, tb, e, err));
-  return launch_check("ns_tile_kernel");
+  return launch_ahead(ns_tile_kernel<A_MN, B_MN>, "ns_tile_kernel", ns_tiles(e, 128) * split, TILE_THREADS, SMEM_BYTES, split, st,
+                      ta, tb, e, err);
 }
 
 // 0: 256 x 256 tiles on SM pairs; else 128 x 128 tiles with K split over that many CTAs.
@@ -745,7 +789,8 @@ int pick_split(const NsArgs& e) {
   if (ns_tiles(e, 256) * 2 >= sms / 2) return 0;
   const int tiles = ns_tiles(e, 128), atoms = (e.K + 63) / 64;
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= sms && atoms >= split * 4) split *= 2;
+  // a split costs the meeting of the shares, about 2 us: taken while each CTA keeps 16 atoms (2 us)
+  while (split < 8 && tiles * split * 2 <= sms && atoms >= split * 32) split *= 2;
   return split;
 }
 
@@ -806,6 +851,7 @@ __device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, float 
 // Partial Gram matrices u u^T in fp64, 4 x 4 of them a thread.
 __global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
   __shared__ float u[CHUNK][TINY + 1];
+  release_next();
   double acc[4][4] = {};
   const int ti = threadIdx.x & 15, tj = threadIdx.x >> 4;
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
@@ -866,6 +912,8 @@ __global__ void __launch_bounds__(1024) muon_tiny_steps_kernel(TinyArgs a) {
   float(*P)[TINY + 1] = A + TINY;
   float(*Q)[TINY + 1] = P + TINY;
   __shared__ double trace[TINY];
+  release_next();
+  wait_for_last();
   const int mm = a.m * a.m;
   double own[4];  // at most 4 elements of the Gram matrix a thread
 #pragma unroll
@@ -912,6 +960,7 @@ __global__ void __launch_bounds__(1024) muon_tiny_steps_kernel(TinyArgs a) {
 __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   __shared__ float u[CHUNK][TINY + 1];
   __shared__ float r[TINY][TINY + 1];
+  wait_for_last();
   for (int e = threadIdx.x; e < TINY * TINY; e += 256) {
     const int i = e / TINY, j = e % TINY;
     r[i][j] = i < a.m && j < a.m ? a.r[i * a.m + j] : 0.f;
@@ -980,10 +1029,12 @@ Walk make_walk(int64_t rows, int64_t cols, int vec) {
   Walk w;
   w.tx_log2 = 8;
   while (w.tx_log2 > 0 && (int64_t(1) << (w.tx_log2 - 1)) * vec >= cols) --w.tx_log2;
-  const int64_t width = (int64_t(1) << w.tx_log2) * vec, height = (256 >> w.tx_log2) * 8;
+  const int64_t width = (int64_t(1) << w.tx_log2) * vec, ty = 256 >> w.tx_log2;
   w.col_tiles = (cols + width - 1) / width;
-  w.tiles = w.col_tiles * ((rows + height - 1) / height);
-  return w;
+  for (w.reps = 8;; w.reps /= 2) {
+    w.tiles = w.col_tiles * ((rows + ty * w.reps - 1) / (ty * w.reps));
+    if (w.reps == 1 || w.tiles >= NORM_PARTS) return w;
+  }
 }
 
 mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
@@ -1004,11 +1055,10 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
   MT_TRY(launch_check("muon_tiny_gram_kernel"));
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel)));
-  muon_tiny_steps_kernel<<<1, 1024, 3 * TINY * (TINY + 1) * 4, st>>>(a);
-  MT_TRY(launch_check("muon_tiny_steps_kernel"));
+  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", 1, 1024, 3 * TINY * (TINY + 1) * 4, 0, st, a));
   const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
-  muon_tiny_apply_kernel<<<static_cast<unsigned>(std::min<int64_t>(chunks, 4 * num_sms())), 256, 0, st>>>(a);
-  return launch_check("muon_tiny_apply_kernel");
+  return launch_ahead(muon_tiny_apply_kernel, "muon_tiny_apply_kernel", static_cast<int>(std::min<int64_t>(chunks, 4 * num_sms())),
+                      256, 0, 0, st, a);
 }
 
 mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
@@ -1024,13 +1074,14 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
   if (v4) {
     muon_norm_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part);
     MT_TRY(launch_check("muon_norm_kernel"));
-    muon_scale_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part, parts, c.eps, p.hi[0], lo, p.ld_x);
+    MT_TRY(launch_ahead(muon_scale_kernel<4>, "muon_scale_kernel", parts, 256, 0, 0, st, g, w, p.part, parts, c.eps, p.hi[0], lo,
+                        p.ld_x));
   } else {
     muon_norm_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part);
     MT_TRY(launch_check("muon_norm_kernel"));
-    muon_scale_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part, parts, c.eps, p.hi[0], lo, p.ld_x);
+    MT_TRY(launch_ahead(muon_scale_kernel<1>, "muon_scale_kernel", parts, 256, 0, 0, st, g, w, p.part, parts, c.eps, p.hi[0], lo,
+                        p.ld_x));
   }
-  MT_TRY(launch_check("muon_scale_kernel"));
   const int m = static_cast<int>(p.m), n = static_cast<int>(p.n);
   const Operand sq_a{p.A, p.ld_a, false, p.m}, sq_p{p.P, p.ld_a, false, p.m};
   for (int s = 0; s < c.steps; ++s) {
