@@ -136,10 +136,11 @@ mt_status launch_ahead(void (*kernel)(Params...), const char* name, int grid, in
   return launch_check(name);
 }
 
-// Writes m' and a partial |u|^2 (fp64) a CTA.
+// Writes m' and a partial |u|^2 (fp64) a CTA; the start of an update, so it also sets the grid barrier back.
 template <int VEC>
-__global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* __restrict__ parts) {
+__global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* __restrict__ parts, unsigned* counter) {
   release_next();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;  // the fused kernel's grid barrier
   double s = 0.0;
   walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
     float g[VEC], m[VEC];
@@ -162,20 +163,19 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* 
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
-// X = S_X u / (|u| + eps) as fp16 head and rest, from g and the m' that the norm pass left.
+// X = S_X u / (|u| + eps) as fp16 head and rest, from g and the m' that the norm pass left. Threads from 256 on
+// only join the sum.
 template <int VEC>
-__global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* __restrict__ parts, int n_parts,
-                                                         double eps, __half* __restrict__ hi, __half* __restrict__ lo,
-                                                         int64_t ld_x) {
-  release_next();
-  wait_for_last();
+__device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const double* __restrict__ parts, int n_parts, double eps,
+                                           __half* __restrict__ hi, __half* __restrict__ lo, int64_t ld_x) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n_parts; i += 256) s += parts[i];
+  for (int i = threadIdx.x; i < n_parts; i += blockDim.x) s += parts[i];
   s = block_sum(s);
   // the factor as a mantissa and two powers of two: u times it stays in fp32's range for any |u|
   int e;
   const float mant = static_cast<float>(frexp(static_cast<double>(S_X) / (sqrt(s) + eps), &e));
   const float p1 = ldexpf(1.f, e / 2), p2 = ldexpf(1.f, e - e / 2);
+  if (threadIdx.x >= 256) return;
   walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
     float g[VEC], m[VEC];
     if (!p.m_in || p.nesterov) ldv<VEC>(g, p.g + row * p.ld_g + col);
@@ -202,6 +202,14 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const d
   });
 }
 
+template <int VEC>
+__global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* __restrict__ parts, int n_parts, double eps,
+                                                         __half* __restrict__ hi, __half* __restrict__ lo, int64_t ld_x) {
+  release_next();
+  wait_for_last();
+  scale_pass<VEC>(p, w, parts, n_parts, eps, hi, lo, ld_x);
+}
+
 // ------------------------------------------------------------------ products
 // v = alpha * (A B^T)[r, c] + beta * (add_hi + add_lo)[r, c] + diag (r == c), stored as fp16 (head, and rest
 // where out_lo is set) or, where out_bf is set, as bf16. Internal matrices have rows of whole 64-element
@@ -218,6 +226,61 @@ struct NsArgs {
   int64_t ld_bf;
   int bf_v16;  // out_bf rows hold 16-byte aligned chunks
 };
+
+// A = X X^T, times S_A.
+__host__ __device__ __forceinline__ NsArgs gram_args(int m, int n, __half* A, int64_t ld_a) {
+  NsArgs e = {};
+  e.M = e.N = m;
+  e.K = n;
+  e.sym = 1;
+  e.alpha = S_A / (S_X * S_X);
+  e.out_hi = A;
+  e.ld_out = ld_a;
+  return e;
+}
+
+// P = b A + c A^2 (fold: + a I), times S_P.
+__host__ __device__ __forceinline__ NsArgs poly_args(int m, const __half* A, __half* P, int64_t ld_a, bool fold) {
+  NsArgs e = {};
+  e.M = e.N = e.K = m;
+  e.sym = 1;
+  e.alpha = NS_C * S_P / (S_A * S_A);
+  e.beta = NS_B * S_P / S_A;
+  e.diag = fold ? NS_A * S_P : 0.f;
+  e.add_hi = A;
+  e.ld_add = ld_a;
+  e.out_hi = P;
+  e.ld_out = ld_a;
+  return e;
+}
+
+// X' = P X (X P in a tall matrix), where P has no a on its diagonal + a X; the last one is the result.
+__host__ __device__ __forceinline__ NsArgs apply_args(int m, int n, bool tall, bool fold, bool last, float scale, const __half* x,
+                                                      const __half* lo, __half* out_hi, __half* out_lo, int64_t ld_x,
+                                                      __nv_bfloat16* o, int64_t ld_o, int bf_v16) {
+  NsArgs e = {};
+  e.M = tall ? n : m;
+  e.N = tall ? m : n;
+  e.K = m;
+  e.raster = tall ? 1 : 2;
+  e.alpha = (last ? scale / S_X : 1.f) / S_P;
+  if (!fold) {
+    e.beta = NS_A;
+    e.add_hi = x;
+    e.add_lo = lo;
+    e.ld_add = ld_x;
+  }
+  if (last) {
+    e.out_bf = o;
+    e.ld_bf = ld_o;
+    e.bf_v16 = bf_v16;
+  } else {
+    e.out_hi = out_hi;
+    e.out_lo = out_lo;
+    e.ld_out = ld_x;
+  }
+  return e;
+}
 
 __device__ __forceinline__ void ld32B(const void* p, uint32_t (&r)[8]) {
   asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -752,6 +815,267 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem_base) : "memory");
 }
 
+// ---------------------------------------------------------------- all steps in one kernel
+// Small matrices spend their time between kernels, not in them: 15 products of a few microseconds. Where each
+// product has no more 128 x 128 tiles than about the GPU has SMs, one cooperative kernel (every CTA resident) runs
+// the scaling and all steps, a grid barrier after each. Tiles as in ns_tile_kernel; the Gram products, whose K is
+// the long side, are split over a cluster of CTAs.
+struct FusedArgs {
+  Grad grad;
+  Walk walk;
+  const double* part;
+  int parts, vec4;
+  double eps;
+  int m, n, tall, steps, two_term, split;  // split: CTAs of a cluster
+  __half *hi[2], *lo, *A, *P;
+  int64_t ld_x, ld_a;
+  float scale;
+  __nv_bfloat16* o;
+  int64_t ld_o;
+  int bf_v16;
+  unsigned* counter;  // zeroed by the norm pass
+};
+
+struct FusedMaps {
+  CUtensorMap x_short[2], x_long[2], A, P;
+};
+
+struct TileSmem {
+  uint8_t *sA, *sB;
+  uint64_t *full, *empty, *tfull;
+  volatile int* abort_flag;
+  uint32_t tmem;
+};
+
+// Everything that the grid's threads wrote is there for its threads' reads and tensor copies afterwards. Bounded
+// like every wait; false: it ran out somewhere, and the kernel ends.
+__device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned target, volatile int* abort_flag, int32_t* err) {
+  asm volatile("fence.proxy.async;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t i = 1;; ++i) {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+      if (v >= target || *abort_flag) break;
+      if ((i & 1023u) == 0 && globaltimer() - t0 > WAIT_NS) {
+        *abort_flag = 1;
+        atomicCAS(err, 0, DEV_ERR_TIMEOUT_PRODUCER);
+        break;
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return *abort_flag == 0;
+}
+
+// One product's tiles: `size` CTAs of the cluster share each tile's K (1: each CTA a tile). it: K atoms that this
+// CTA's ring has carried; tiles: tiles it has finished (the parity of tfull).
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUtensorMap* tmB, const NsArgs& ep, int size,
+                                              const TileSmem& sm, uint32_t& it, uint32_t& tiles, int32_t* err) {
+  constexpr int STAGES = ATOMS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = size > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int num_m = (ep.M + 127) / 128, num_n = (ep.N + 127) / 128;
+  const int num_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
+  const int atoms = (ep.K + 63) / 64;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * rank / size);
+  const int nk = static_cast<int>(static_cast<int64_t>(atoms) * (rank + 1) / size) - kb0;
+  const int in_tile = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
+  const int share16 = 8 / size, count = share16 >= 2 ? share16 / 2 : (half == 0 ? share16 : 0);
+  for (int t = static_cast<int>(blockIdx.x) / size; t < num_tiles; t += static_cast<int>(gridDim.x) / size) {
+    int mb, nb;
+    ns_tile(ep, t, num_m, num_n, mb, nb);
+    const int first_col = nb * 128 + rank * (128 / size) + half * count * 16, row = mb * 128 + in_tile;
+    const bool mirror = ep.sym && mb != nb;
+    Addend add[4];
+    bool done = true;
+    if (warp == 0) {
+      const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
+      for (int i = 0; i < nk; ++i) {
+        const uint32_t g = it + i, s = g % STAGES;
+        if (!warp_wait(smem_u32(&sm.empty[s]), ((g / STAGES) & 1u) ^ 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
+        if (lane == 0) {
+          const uint32_t fb = smem_u32(&sm.full[s]);
+          mbar_expect_tx(fb, bytes);
+          load_atom<A_MN>(smem_u32(sm.sA + s * HALF), MN_BOX, mb * 128, ep.M, (kb0 + i) * 64,
+                          [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmA, fb, c0, c1); });
+          load_atom<B_MN>(smem_u32(sm.sB + s * HALF), MN_BOX, nb * 128, ep.N, (kb0 + i) * 64,
+                          [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmB, fb, c0, c1); });
+        }
+        __syncwarp();
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
+      bool ok = true;
+      for (int i = 0; i < nk; ++i) {
+        const uint32_t g = it + i, s = g % STAGES;
+        if (!warp_wait(smem_u32(&sm.full[s]), (g / STAGES) & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        if (lane == 0) {
+          const uint32_t a_base = smem_u32(sm.sA + s * HALF), b_base = smem_u32(sm.sB + s * HALF);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(sm.tmem, step_desc<A_MN, 1>(a_base, kk), step_desc<B_MN, 1>(b_base, kk), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(smem_u32(&sm.empty[s]));
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) umma_commit(smem_u32(sm.tfull));
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < count) load_addend(ep, row, first_col + 16 * c, add[c]);
+      done = warp_wait(smem_u32(sm.tfull), tiles & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
+      fence_after();
+      if (done) {
+        const uint32_t tbase = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
+          if (size == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col0 = first_col + c * 32 + 16 * h;
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
+              if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror);
+            }
+          } else {
+            float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(sm.sA) + in_tile * RED_LD + half * 64 + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              p[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                                 __uint_as_float(r[4 * i + 3]));
+          }
+        }
+      }
+    }
+    it += static_cast<uint32_t>(nk);
+    ++tiles;
+    fence_before();
+    if (size > 1) {
+      cluster_sync();  // the cluster's tiles are in shared memory
+      if (warp >= 2 && done) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col0 = first_col + 16 * c;
+          if (c < count && col0 < ep.N) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+            const uint32_t at = smem_u32(sm.sA) + (in_tile * RED_LD + (col0 - nb * 128)) * 4;
+            for (int p = 0; p < size; p += 2) {
+              float4 f[2][4];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t from = map_to_rank(at, static_cast<uint32_t>(p + q));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                               : "=f"(f[q][i].x), "=f"(f[q][i].y), "=f"(f[q][i].z), "=f"(f[q][i].w)
+                               : "r"(from + 16 * i)
+                               : "memory");
+              }
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  v[4 * i] += f[q][i].x;
+                  v[4 * i + 1] += f[q][i].y;
+                  v[4 * i + 2] += f[q][i].z;
+                  v[4 * i + 3] += f[q][i].w;
+                }
+            }
+            finish16(ep, row, col0, v, add[c], mirror);
+          }
+        }
+      }
+      fence_proxy_async_smem();  // the ring takes tensor copies again where the tile was
+      cluster_sync();
+    } else {
+      __syncthreads();  // the accumulator is read
+    }
+    fence_after();
+  }
+}
+
+template <bool TALL>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    ns_fused_kernel(const __grid_constant__ FusedMaps maps, const __grid_constant__ FusedArgs a, int32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TileSmem sm;
+  sm.sA = smem;
+  sm.sB = smem + ATOMS * HALF;
+  sm.full = reinterpret_cast<uint64_t*>(smem + RING);
+  sm.empty = sm.full + ATOMS;
+  sm.tfull = sm.empty + ATOMS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.tfull + 1);
+  sm.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ATOMS; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    mbar_init(smem_u32(sm.tfull), 1);
+    *sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  sm.tmem = *tmem_slot;
+  wait_for_last();
+  if (a.vec4)
+    scale_pass<4>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
+  else
+    scale_pass<1>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
+  uint32_t it = 0, tiles = 0;
+  unsigned target = gridDim.x;
+  bool ok = grid_barrier(a.counter, target, sm.abort_flag, err);
+  for (int s = 0; s < a.steps && ok; ++s) {
+    const __half* x = a.hi[s & 1];
+    const bool fold = s >= a.two_term, last = s + 1 == a.steps;
+    NsArgs e = gram_args(a.m, a.n, a.A, a.ld_a);
+    fused_product<TALL, TALL>(&maps.x_short[s & 1], &maps.x_short[s & 1], e, a.split, sm, it, tiles, err);
+    ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
+    if (!ok) break;
+    e = poly_args(a.m, a.A, a.P, a.ld_a, fold);
+    fused_product<false, false>(&maps.A, &maps.A, e, 1, sm, it, tiles, err);
+    ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
+    if (!ok) break;
+    e = apply_args(a.m, a.n, TALL, fold, last, a.scale, x, a.lo, a.hi[(s + 1) & 1], s + 1 < a.two_term ? a.lo : nullptr, a.ld_x,
+                   a.o, a.ld_o, a.bf_v16);
+    if (TALL)
+      fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, sm, it, tiles, err);
+    else
+      fused_product<false, true>(&maps.P, &maps.x_long[s & 1], e, 1, sm, it, tiles, err);
+    if (!last) ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
+  }
+  fence_before();
+  __syncthreads();
+  if (cluster_size() > 1) cluster_sync();
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(sm.tmem) : "memory");
+}
+
 // An fp16 operand: element (r, k) at p[r * ld + k] (K-major) or p[k * ld + r] (MN-major).
 struct Operand {
   const __half* p;
@@ -794,15 +1118,26 @@ int pick_split(const NsArgs& e) {
   return split;
 }
 
-mt_status ns_product(const Operand& a, const Operand& b, const NsArgs& e, cudaStream_t st) {
-  CUtensorMap ta, tb;
-  MT_TRY(operand_map(&ta, a, e.K));
-  MT_TRY(operand_map(&tb, b, e.K));
+mt_status ns_product(const CUtensorMap& ta, bool a_mn, const CUtensorMap& tb, bool b_mn, const NsArgs& e, cudaStream_t st) {
   const int split = pick_split(e);
-  add_exec_flops(2.0 * double(e.M) * double(e.N) * double(e.K) * (e.sym ? 0.5 : 1.0));
-  if (!a.mn && !b.mn) return ns_launch<false, false>(ta, tb, e, split, st);
-  if (!a.mn) return ns_launch<false, true>(ta, tb, e, split, st);
+  if (!a_mn && !b_mn) return ns_launch<false, false>(ta, tb, e, split, st);
+  if (!a_mn) return ns_launch<false, true>(ta, tb, e, split, st);
   return ns_launch<true, true>(ta, tb, e, split, st);
+}
+
+// Whether all steps run as one kernel: each product's tiles fit the GPU about once, so that whole SM pairs on
+// 256 x 256 tiles would not be faster.
+bool pick_fused(int m, int n) {
+  const int64_t tm = (m + 127) / 128, tn = (n + 127) / 128;
+  return tm * tn <= num_sms() && tm * (tm + 1) / 2 <= num_sms();
+}
+
+// CTAs that share K of a Gram product in the fused kernel (its cluster size).
+int fused_split(int m, int n) {
+  const int tm = (m + 127) / 128, tiles = tm * (tm + 1) / 2, atoms = (n + 63) / 64;
+  int split = 1;
+  while (split < 4 && tiles * split * 2 <= num_sms() && atoms >= split * 16) split *= 2;
+  return split;
 }
 
 // ------------------------------------------------------------------ short side of at most 64
@@ -996,6 +1331,7 @@ struct Plan {
   int64_t m, n, ld_x, ld_a;
   int parts;
   double* part;
+  unsigned* counter;
   __half *hi[2], *lo, *A, *P;
   double* gram;
   float* r;
@@ -1016,6 +1352,7 @@ Plan plan(int64_t rows, int64_t cols, void* ws) {
     p.ld_x = align_up(cols, 64);
     p.ld_a = align_up(p.m, 64);
     p.part = b.take<double>(NORM_PARTS);
+    p.counter = b.take<unsigned>(1);
     for (auto& h : p.hi) h = b.take<__half>(rows * p.ld_x);
     p.lo = b.take<__half>(rows * p.ld_x);
     p.A = b.take<__half>(p.m * p.ld_a);
@@ -1061,6 +1398,49 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
                       256, 0, 0, st, a);
 }
 
+template <bool TALL>
+mt_status fused_launch(const FusedMaps& maps, const FusedArgs& a, cudaStream_t st) {
+  int32_t* err = device_error_word();
+  if (!err) return fail(MT_ERR_CUDA, "device error word unavailable");
+  static SmemOptIn opt;
+  MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_fused_kernel<TALL>)));
+  // a CTA for each tile of the largest product, whole clusters, all resident
+  const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128;
+  const int want = std::max(tm * tn, tm * (tm + 1) / 2 * a.split);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min((want + a.split - 1) / a.split, num_sms() / a.split) * a.split), 1, 1);
+  cfg.blockDim = dim3(TILE_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (a.split > 1) {
+    // clusters lie within a GPC: fewer of them may be resident at once than SMs suggest (asked once a device)
+    static std::atomic<int> cache[64][2];
+    int dev = 0, most = 0;
+    MT_CUDA(cudaGetDevice(&dev));
+    std::atomic<int>* known = dev < 64 ? &cache[dev][a.split == 2 ? 0 : 1] : nullptr;
+    if (known) most = known->load(std::memory_order_relaxed);
+    if (most == 0) {
+      cudaLaunchConfig_t full = cfg;
+      full.gridDim.x = static_cast<unsigned>(num_sms() / a.split * a.split);
+      MT_CUDA(cudaOccupancyMaxActiveClusters(&most, ns_fused_kernel<TALL>, &full));
+      if (most < 1) return fail(MT_ERR_CUDA, "ns_fused_kernel: no cluster of %d fits the device", a.split);
+      if (known) known->store(most, std::memory_order_relaxed);
+    }
+    cfg.gridDim.x = std::min<unsigned>(cfg.gridDim.x, static_cast<unsigned>(most * a.split));
+  }
+  MT_CUDA(cudaLaunchKernelEx(&cfg, ns_fused_kernel<TALL>, maps, a, err));
+  return launch_check("ns_fused_kernel");
+}
+
 mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
   const bool tall = g.rows > g.cols;
   auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
@@ -1069,67 +1449,68 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
   const Walk w = make_walk(g.rows, g.cols, v4 ? 4 : 1);
   const int parts = static_cast<int>(std::min<int64_t>(w.tiles, NORM_PARTS));
   // a two-term X for all steps but the last two
-  const int two_term = c.steps - 2;
+  const int two_term = c.steps - 2, m = static_cast<int>(p.m), n = static_cast<int>(p.n);
   __half* lo = two_term > 0 ? p.lo : nullptr;
-  if (v4) {
-    muon_norm_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part);
-    MT_TRY(launch_check("muon_norm_kernel"));
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(o);
+  const int bf_v16 = a16(o) && ld_o % 8 == 0;
+  // X with the short or the long side as rows: K-major or MN-major by the matrix's orientation
+  FusedMaps maps;
+  for (int i = 0; i < 2; ++i) {
+    MT_TRY(operand_map(&maps.x_short[i], Operand{p.hi[i], p.ld_x, tall, p.m}, n));
+    MT_TRY(operand_map(&maps.x_long[i], Operand{p.hi[i], p.ld_x, !tall, p.n}, m));
+  }
+  MT_TRY(operand_map(&maps.A, Operand{p.A, p.ld_a, false, p.m}, m));
+  MT_TRY(operand_map(&maps.P, Operand{p.P, p.ld_a, false, p.m}, m));
+  const double mm = static_cast<double>(m) * m;
+  add_exec_flops(2.0 * c.steps * (0.5 * mm * n + 0.5 * mm * m + mm * n));
+
+  if (v4)
+    muon_norm_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part, p.counter);
+  else
+    muon_norm_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part, p.counter);
+  MT_TRY(launch_check("muon_norm_kernel"));
+  if (pick_fused(m, n)) {
+    FusedArgs a;
+    a.grad = g;
+    a.walk = w;
+    a.part = p.part;
+    a.parts = parts;
+    a.vec4 = v4;
+    a.eps = c.eps;
+    a.m = m;
+    a.n = n;
+    a.tall = tall;
+    a.steps = c.steps;
+    a.two_term = two_term;
+    a.split = fused_split(m, n);
+    a.hi[0] = p.hi[0];
+    a.hi[1] = p.hi[1];
+    a.lo = p.lo;
+    a.A = p.A;
+    a.P = p.P;
+    a.ld_x = p.ld_x;
+    a.ld_a = p.ld_a;
+    a.scale = c.scale;
+    a.o = out;
+    a.ld_o = ld_o;
+    a.bf_v16 = bf_v16;
+    a.counter = p.counter;
+    return tall ? fused_launch<true>(maps, a, st) : fused_launch<false>(maps, a, st);
+  }
+  if (v4)
     MT_TRY(launch_ahead(muon_scale_kernel<4>, "muon_scale_kernel", parts, 256, 0, 0, st, g, w, p.part, parts, c.eps, p.hi[0], lo,
                         p.ld_x));
-  } else {
-    muon_norm_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part);
-    MT_TRY(launch_check("muon_norm_kernel"));
+  else
     MT_TRY(launch_ahead(muon_scale_kernel<1>, "muon_scale_kernel", parts, 256, 0, 0, st, g, w, p.part, parts, c.eps, p.hi[0], lo,
                         p.ld_x));
-  }
-  const int m = static_cast<int>(p.m), n = static_cast<int>(p.n);
-  const Operand sq_a{p.A, p.ld_a, false, p.m}, sq_p{p.P, p.ld_a, false, p.m};
   for (int s = 0; s < c.steps; ++s) {
     const bool fold = s >= two_term, last = s + 1 == c.steps;
-    const __half* x = p.hi[s & 1];
-    // A = X X^T (X^T X): the short side's rows of X are K-major in a wide matrix, MN-major in a tall one
-    NsArgs e = {};
-    const Operand short_side{x, p.ld_x, tall, p.m};
-    e.M = e.N = m;
-    e.K = n;
-    e.sym = 1;
-    e.alpha = S_A / (S_X * S_X);
-    e.out_hi = p.A;
-    e.ld_out = p.ld_a;
-    MT_TRY(ns_product(short_side, short_side, e, st));
-    // P = b A + c A^2 (+ a I)
-    e.K = m;
-    e.alpha = NS_C * S_P / (S_A * S_A);
-    e.beta = NS_B * S_P / S_A;
-    e.diag = fold ? NS_A * S_P : 0.f;
-    e.add_hi = p.A;
-    e.ld_add = p.ld_a;
-    e.out_hi = p.P;
-    MT_TRY(ns_product(sq_a, sq_a, e, st));
-    // X' = P X (+ a X), the long side of X as rows: MN-major in a wide matrix, K-major in a tall one
-    e = {};
-    const Operand long_side{x, p.ld_x, !tall, p.n};
-    e.M = tall ? n : m;
-    e.N = tall ? m : n;
-    e.K = m;
-    e.raster = tall ? 1 : 2;
-    e.alpha = (last ? c.scale / S_X : 1.f) / S_P;
-    if (!fold) {
-      e.beta = NS_A;
-      e.add_hi = x;
-      e.add_lo = p.lo;
-      e.ld_add = p.ld_x;
-    }
-    if (last) {
-      e.out_bf = reinterpret_cast<__nv_bfloat16*>(o);
-      e.ld_bf = ld_o;
-      e.bf_v16 = a16(o) && ld_o % 8 == 0;
-    } else {
-      e.out_hi = p.hi[(s + 1) & 1];
-      e.out_lo = s + 1 < two_term ? p.lo : nullptr;
-      e.ld_out = p.ld_x;
-    }
-    MT_TRY(tall ? ns_product(long_side, sq_p, e, st) : ns_product(sq_p, long_side, e, st));
+    const CUtensorMap &xs = maps.x_short[s & 1], &xl = maps.x_long[s & 1];
+    MT_TRY(ns_product(xs, tall, xs, tall, gram_args(m, n, p.A, p.ld_a), st));
+    MT_TRY(ns_product(maps.A, false, maps.A, false, poly_args(m, p.A, p.P, p.ld_a, fold), st));
+    const NsArgs e = apply_args(m, n, tall, fold, last, c.scale, p.hi[s & 1], p.lo, p.hi[(s + 1) & 1],
+                                s + 1 < two_term ? p.lo : nullptr, p.ld_x, out, ld_o, bf_v16);
+    MT_TRY(tall ? ns_product(xl, false, maps.P, false, e, st) : ns_product(maps.P, false, xl, true, e, st));
   }
   return MT_OK;
 }
