@@ -49,12 +49,12 @@ int num_sms() {
   return cache[dev];
 }
 
-mt_status SmemOptIn::raise(const void* kernel) {
+mt_status SmemOptIn::raise(const void* kernel, int bytes) {
   int dev = 0;
   MT_CUDA(cudaGetDevice(&dev));
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (bit && (done_.load(std::memory_order_acquire) & bit)) return MT_OK;
-  MT_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024));
+  MT_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
   done_.fetch_or(bit, std::memory_order_release);
   return MT_OK;
 }

@@ -47,10 +47,10 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 // Number of SMs of the current device (cached per device).
 int num_sms();
 
-// Lets a kernel use up to 224 KiB of dynamic shared memory, once on each device (one static object a kernel).
+// Lets a kernel use up to `bytes` of dynamic shared memory, once on each device (one static object a kernel).
 class SmemOptIn {
  public:
-  mt_status raise(const void* kernel);
+  mt_status raise(const void* kernel, int bytes = 224 * 1024);
 
  private:
   std::atomic<uint64_t> done_{0};  // bit d: device d

@@ -22,7 +22,7 @@
 // |u|_F is summed in fp64, so that no magnitude of g that fp32 holds over- or underflows.
 //
 // Matrices whose short side is at most 64 take no tensor cores: their Gram matrix (in fp64) is all that the
-// steps need, one CTA runs them on it in fp32, and the result is one product with u: three launches.
+// steps need, one CTA runs them on it in fp32, and the result is one product with u: four launches.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -71,26 +71,29 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-// The passes over the matrix walk tiles of (256 / tx) * reps rows and tx * VEC columns, tx a power of two that
-// fits narrow matrices, VEC = 4 where rows are 16-byte aligned, reps up to 8 (fewer in small matrices).
+// The passes over the matrix walk tiles of (256 / tx) * REPS rows and tx * VEC columns, tx a power of two that
+// fits narrow matrices, VEC = 4 where rows are 16-byte aligned. A thread's REPS rows are in flight together.
+constexpr int REPS = 8;
 struct Walk {
-  int tx_log2, reps;
+  int tx_log2;
   int64_t col_tiles, tiles;
 };
 
-template <int VEC, class F>
-__device__ __forceinline__ void walk(const Walk& w, int64_t rows, int64_t cols, F&& f) {
+// load(k, row, col) for the thread's rows, then use(k, row, col).
+template <int VEC, class L, class F>
+__device__ __forceinline__ void walk(const Walk& w, int64_t rows, int64_t cols, L&& load, F&& use) {
   const int tx = 1 << w.tx_log2, ty = 256 >> w.tx_log2;
   const int x = threadIdx.x & (tx - 1), y = threadIdx.x >> w.tx_log2;
   for (int64_t tl = blockIdx.x; tl < w.tiles; tl += gridDim.x) {
     const int64_t rt = tl / w.col_tiles, ct = tl - rt * w.col_tiles;
-    const int64_t col = (ct * tx + x) * VEC;
+    const int64_t col = (ct * tx + x) * VEC, row0 = rt * (REPS * ty) + y;
     if (col >= cols) continue;
-#pragma unroll 4
-    for (int k = 0; k < w.reps; ++k) {
-      const int64_t row = rt * (w.reps * ty) + k * ty + y;
-      if (row < rows) f(row, col);
-    }
+#pragma unroll
+    for (int k = 0; k < REPS; ++k)
+      if (row0 + k * ty < rows) load(k, row0 + k * ty, col);
+#pragma unroll
+    for (int k = 0; k < REPS; ++k)
+      if (row0 + k * ty < rows) use(k, row0 + k * ty, col);
   }
 }
 
@@ -142,23 +145,27 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* 
   release_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;  // the fused kernel's grid barrier
   double s = 0.0;
-  walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
-    float g[VEC], m[VEC];
-    ldv<VEC>(g, p.g + row * p.ld_g + col);
-    if (p.m_in) {
-      ldv<VEC>(m, p.m_in + row * p.ld_m + col);
+  float g[REPS][VEC], m[REPS][VEC];
+  walk<VEC>(
+      w, p.rows, p.cols,
+      [&](int k, int64_t row, int64_t col) {
+        ldv<VEC>(g[k], p.g + row * p.ld_g + col);
+        if (p.m_in) ldv<VEC>(m[k], p.m_in + row * p.ld_m + col);
+      },
+      [&](int k, int64_t row, int64_t col) {
+        if (p.m_in) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        float mo;
-        g[i] = momentum_step(p, g[i], m[i], mo);
-        m[i] = mo;
-      }
-      *reinterpret_cast<typename F32<VEC>::type*>(p.m_out + row * p.ld_m + col) =
-          *reinterpret_cast<typename F32<VEC>::type*>(m);
-    }
+          for (int i = 0; i < VEC; ++i) {
+            float mo;
+            g[k][i] = momentum_step(p, g[k][i], m[k][i], mo);
+            m[k][i] = mo;
+          }
+          *reinterpret_cast<typename F32<VEC>::type*>(p.m_out + row * p.ld_m + col) =
+              *reinterpret_cast<typename F32<VEC>::type*>(m[k]);
+        }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s = fma(static_cast<double>(g[i]), static_cast<double>(g[i]), s);
-  });
+        for (int i = 0; i < VEC; ++i) s = fma(static_cast<double>(g[k][i]), static_cast<double>(g[k][i]), s);
+      });
   s = block_sum(s);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
@@ -176,30 +183,31 @@ __device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const d
   const float mant = static_cast<float>(frexp(static_cast<double>(S_X) / (sqrt(s) + eps), &e));
   const float p1 = ldexpf(1.f, e / 2), p2 = ldexpf(1.f, e - e / 2);
   if (threadIdx.x >= 256) return;
-  walk<VEC>(w, p.rows, p.cols, [&](int64_t row, int64_t col) {
-    float g[VEC], m[VEC];
-    if (!p.m_in || p.nesterov) ldv<VEC>(g, p.g + row * p.ld_g + col);
-    if (p.m_in) {
-      ldv<VEC>(m, p.m_out + row * p.ld_m + col);
+  float g[REPS][VEC], m[REPS][VEC];
+  walk<VEC>(
+      w, p.rows, p.cols,
+      [&](int k, int64_t row, int64_t col) {
+        if (!p.m_in || p.nesterov) ldv<VEC>(g[k], p.g + row * p.ld_g + col);
+        if (p.m_in) ldv<VEC>(m[k], p.m_out + row * p.ld_m + col);
+      },
+      [&](int k, int64_t row, int64_t col) {
+        __half h[VEC], l[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) g[i] = p.nesterov ? fmaf(p.mu, m[i], g[i]) : m[i];
-    }
-    __half h[VEC], l[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float v = g[i] * mant * p1 * p2;
-      h[i] = __float2half_rn(v);
-      l[i] = __float2half_rn(v - __half2float(h[i]));
-    }
-    const int64_t at = row * ld_x + col;
-    if constexpr (VEC == 4) {
-      *reinterpret_cast<uint2*>(hi + at) = *reinterpret_cast<uint2*>(h);
-      if (lo) *reinterpret_cast<uint2*>(lo + at) = *reinterpret_cast<uint2*>(l);
-    } else {
-      hi[at] = h[0];
-      if (lo) lo[at] = l[0];
-    }
-  });
+        for (int i = 0; i < VEC; ++i) {
+          const float u = !p.m_in ? g[k][i] : p.nesterov ? fmaf(p.mu, m[k][i], g[k][i]) : m[k][i];
+          const float v = u * mant * p1 * p2;
+          h[i] = __float2half_rn(v);
+          l[i] = __float2half_rn(v - __half2float(h[i]));
+        }
+        const int64_t at = row * ld_x + col;
+        if constexpr (VEC == 4) {
+          *reinterpret_cast<uint2*>(hi + at) = *reinterpret_cast<uint2*>(h);
+          if (lo) *reinterpret_cast<uint2*>(lo + at) = *reinterpret_cast<uint2*>(l);
+        } else {
+          hi[at] = h[0];
+          if (lo) lo[at] = l[0];
+        }
+      });
 }
 
 template <int VEC>
@@ -313,14 +321,31 @@ __device__ __forceinline__ void load_addend(const NsArgs& e, int row, int col0, 
   }
 }
 
-// Epilogue of 16 columns of the 32 rows that a warp holds, one row a lane (all lanes call it).
-__device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, float (&v)[16], const Addend& a, bool mirror) {
+// Epilogue of 16 columns of the 32 rows that a warp holds, one row a lane (all lanes call it). stage: 32 x STAGE_LD
+// bf16 of shared memory of the warp's own, for results whose rows have no 16-byte alignment: from there they are
+// written two rows at a time, neighbouring lanes to neighbouring elements.
+constexpr int STAGE_LD = 18;
+constexpr int STAGE_BYTES = 32 * STAGE_LD * 2;
+__device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, float (&v)[16], const Addend& a, bool mirror,
+                                         uint16_t* stage) {
   const bool live = row < e.M;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 h = h2f(a.hi[i]), l = h2f(a.lo[i]);
-    v[2 * i] = fmaf(e.beta, l.x, fmaf(e.beta, h.x, v[2 * i] * e.alpha));
-    v[2 * i + 1] = fmaf(e.beta, l.y, fmaf(e.beta, h.y, v[2 * i + 1] * e.alpha));
+  for (int i = 0; i < 16; ++i) v[i] *= e.alpha;
+  if (e.add_hi) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 h = h2f(a.hi[i]);
+      v[2 * i] = fmaf(e.beta, h.x, v[2 * i]);
+      v[2 * i + 1] = fmaf(e.beta, h.y, v[2 * i + 1]);
+    }
+  }
+  if (e.add_lo) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 l = h2f(a.lo[i]);
+      v[2 * i] = fmaf(e.beta, l.x, v[2 * i]);
+      v[2 * i + 1] = fmaf(e.beta, l.y, v[2 * i + 1]);
+    }
   }
   if (e.diag != 0.f) {
 #pragma unroll
@@ -328,21 +353,29 @@ __device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, flo
       if (row == col0 + i) v[i] += e.diag;
   }
   if (e.out_bf) {
-    if (!live) return;
-    __nv_bfloat16* o = e.out_bf + static_cast<int64_t>(row) * e.ld_bf + col0;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
     if (e.bf_v16 && col0 + 16 <= e.N) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint4 u;
-        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
-        reinterpret_cast<uint4*>(o)[q] = u;
+      uint4* o = reinterpret_cast<uint4*>(e.out_bf + static_cast<int64_t>(row) * e.ld_bf + col0);
+      if (live) {
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     } else {
+      const int lane = threadIdx.x & 31;
+      uint32_t* mine = reinterpret_cast<uint32_t*>(stage + lane * STAGE_LD);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (col0 + i < e.N) o[i] = __float2bfloat16_rn(v[i]);
+      for (int i = 0; i < 8; ++i) mine[i] = w[i];
+      __syncwarp();
+      const int c = lane & 15, row0 = row - lane;
+      for (int r = lane >> 4; r < 32; r += 2)
+        if (row0 + r < e.M && col0 + c < e.N)
+          reinterpret_cast<uint16_t*>(e.out_bf)[static_cast<int64_t>(row0 + r) * e.ld_bf + col0 + c] = stage[r * STAGE_LD + c];
+      __syncwarp();
     }
     return;
   }
@@ -401,7 +434,7 @@ constexpr int HALF = 128 * 64 * 2;    // 16 KiB: 128 rows of one operand, one 64
 constexpr int MN_BOX = 64 * 64 * 2;   // one 64 x 64 MN-major box
 constexpr int ATOMS = 6;              // K atoms of both operands that a CTA's ring holds: 192 KiB
 constexpr int RING = ATOMS * 2 * HALF;
-constexpr int SMEM_BYTES = RING + 256 + 1024;
+constexpr int SMEM_BYTES = RING + 256 + 4 * STAGE_BYTES + 1024;
 constexpr int NS_THREADS = 192;       // TMA warp, MMA warp, four epilogue warps
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -422,6 +455,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+
+// One thread's bounded wait, the usual case inline (a role that is one thread needs no warp-wide agreement).
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* err, int code) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, err, code);
 }
 
 // Instruction descriptor of kind::f16 with fp16 operands and fp32 sums.
@@ -449,12 +488,17 @@ __device__ __forceinline__ void load_atom(uint32_t dst, int mn_stride, int r0, i
   }
 }
 
-// Descriptor of K step kk (16 wide) of a stage of KA atoms: K-major, atom kk / 4 and 32 bytes a step inside the
-// swizzled rows; MN-major, 16 rows of K (2 KiB) a step, the two 64-row halves KA boxes apart.
+// Descriptor of a stage of KA atoms at `base`, and how far K step kk (16 wide) lies into it, in the descriptor's
+// 16-byte units (added to its low word: one add a product, where building each would hold up the issuing thread).
+// K-major: atom kk / 4 and 32 bytes a step inside the swizzled rows; MN-major: 16 rows of K (2 KiB) a step, the two
+// 64-row halves KA boxes apart.
 template <bool MN, int KA>
-__device__ __forceinline__ uint64_t step_desc(uint32_t base, int kk) {
-  return MN ? smem_desc(base + kk * 2048, KA * MN_BOX, 1024)
-            : smem_desc(base + (kk >> 2) * HALF + (kk & 3) * 32, 16, 1024);
+__device__ __forceinline__ uint64_t stage_desc(uint32_t base) {
+  return MN ? smem_desc(base, KA * MN_BOX, 1024) : smem_desc(base, 16, 1024);
+}
+template <bool MN>
+__device__ __forceinline__ constexpr uint64_t step_off(int kk) {
+  return static_cast<uint64_t>(MN ? kk * 2048 : (kk >> 2) * HALF + (kk & 3) * 32) >> 4;
 }
 
 // ---------------------------------------------------------------- 256 x 256 tiles on two SMs
@@ -574,14 +618,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
           fence_after();
           if (lane == 0) {
-            const uint32_t a_base = smem_u32(sA + s * OP_STAGE), b_base = smem_u32(sB + s * OP_STAGE);
+            const uint64_t ad = stage_desc<A_MN, KA>(smem_u32(sA + s * OP_STAGE)), bd = stage_desc<B_MN, KA>(smem_u32(sB + s * OP_STAGE));
             const int ksteps = 4 * min(KA, (ep.K - kb * BK + 63) / 64);
             for (int kk = 0; kk < ksteps; ++kk)
               asm volatile(
                   "{\n\t.reg .pred p;\n\t"
                   "setp.ne.b32 p, %4, 0;\n\t"
                   "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                  "l"(step_desc<A_MN, KA>(a_base, kk)), "l"(step_desc<B_MN, KA>(b_base, kk)), "r"(idesc),
+                  "l"(ad + step_off<A_MN>(kk)), "l"(bd + step_off<B_MN>(kk)), "r"(idesc),
                   "r"((kb > 0 || kk > 0) ? 1u : 0u));
             commit(&empty[s]);
           }
@@ -594,6 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     }
   } else {
     const int q = warp & 3;  // TMEM lanes [32 q, 32 q + 32)
+    uint16_t* stage = reinterpret_cast<uint16_t*>(smem + RING + 256 + q * STAGE_BYTES);
     int tl = 0;
     for (int t = cluster; t < num_tiles; t += n_clusters, ++tl) {
       const int ab = tl & 1;
@@ -617,7 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
-          finish16(ep, row, col0 + 16 * h, v, add[h], ep.sym && mb != nb);
+          finish16(ep, row, col0 + 16 * h, v, add[h], ep.sym && mb != nb, stage);
         }
       }
       fence_before();
@@ -699,14 +744,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const int first_col = nb * 128 + rank * (128 / size) + half * count * 16;
   const int row = mb * 128 + in_tile;
   const bool mirror = ep.sym && mb != nb;
+  uint16_t* stage = reinterpret_cast<uint16_t*>(smem + 128 * RED_LD * 4 + max(warp - 2, 0) * STAGE_BYTES);  // the ring is read by then
   Addend add[4];
   bool done = true;  // this warp's waits all ended
   if (warp == 0) {
-    const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const int it = kb - kb0, s = it % STAGES;
-      if (!warp_wait(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
-      if (lane == 0) {
+    if (lane == 0) {
+      const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int it = kb - kb0, s = it % STAGES;
+        if (!wait_one(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
         const uint32_t fb = smem_u32(&full[s]);
         mbar_expect_tx(fb, bytes);
         load_atom<A_MN>(smem_u32(sA + s * HALF), MN_BOX, mb * 128, ep.M, kb * 64,
@@ -714,29 +760,28 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         load_atom<B_MN>(smem_u32(sB + s * HALF), MN_BOX, nb * 128, ep.N, kb * 64,
                         [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, &tmB, fb, c0, c1); });
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
-    bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const int it = kb - kb0, s = it % STAGES;
-      if (!warp_wait(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
-        ok = false;
-        break;
-      }
-      fence_after();
-      if (lane == 0) {
-        const uint32_t a_base = smem_u32(sA + s * HALF), b_base = smem_u32(sB + s * HALF);
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
+      const uint64_t a_desc = stage_desc<A_MN, 1>(smem_u32(sA)), b_desc = stage_desc<B_MN, 1>(smem_u32(sB));
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int it = kb - kb0, s = it % STAGES;
+        if (!wait_one(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint64_t ad = a_desc + s * (HALF >> 4), bd = b_desc + s * (HALF >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem_base, step_desc<A_MN, 1>(a_base, kk), step_desc<B_MN, 1>(b_base, kk), idesc,
-                    (it > 0 || kk > 0) ? 1u : 0u);
+          umma_bf16(tmem_base, ad + step_off<A_MN>(kk), bd + step_off<B_MN>(kk), idesc, (it > 0 || kk > 0) ? 1u : 0u);
         umma_commit(smem_u32(&empty[s]));
       }
-      __syncwarp();
+      if (ok) umma_commit(smem_u32(tfull));
     }
-    if (ok && lane == 0) umma_commit(smem_u32(tfull));
     __syncwarp();
   } else {
 #pragma unroll
@@ -757,7 +802,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
-            if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror);
+            if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror, stage);
           }
         } else {
           // every product that read the ring has completed: the tile may overlay it
@@ -805,7 +850,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 v[4 * i + 3] += f[q][i].w;
               }
           }
-          finish16(ep, row, col0, v, add[c], mirror);
+          finish16(ep, row, col0, v, add[c], mirror, stage);
         }
       }
     }
@@ -840,9 +885,14 @@ struct FusedMaps {
   CUtensorMap x_short[2], x_long[2], A, P;
 };
 
+constexpr int FUSED_ATOMS = 5;                      // K atoms of the ring: 160 KiB
+constexpr int FUSED_RING = FUSED_ATOMS * 2 * HALF;  // its start holds a CTA's shares while they are sent
+constexpr int SHARES = 128 * 128 * 4;               // the shares that a CTA receives: an fp32 tile in all
+constexpr int FUSED_SMEM = FUSED_RING + SHARES + 256 + 1024;
+
 struct TileSmem {
-  uint8_t *sA, *sB;
-  uint64_t *full, *empty, *tfull;
+  uint8_t *sA, *sB, *recv;
+  uint64_t *full, *empty, *tfull, *rfull;
   volatile int* abort_flag;
   uint32_t tmem;
 };
@@ -850,15 +900,15 @@ struct TileSmem {
 // Everything that the grid's threads wrote is there for its threads' reads and tensor copies afterwards. Bounded
 // like every wait; false: it ran out somewhere, and the kernel ends.
 __device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned target, volatile int* abort_flag, int32_t* err) {
-  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(counter, 1u);
+    __threadfence();  // cumulative: releases what the CTA's threads wrote before the barrier above
+    asm volatile("red.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
     const unsigned long long t0 = globaltimer();
     for (uint32_t i = 1;; ++i) {
       unsigned v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+      asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
       if (v >= target || *abort_flag) break;
       if ((i & 1023u) == 0 && globaltimer() - t0 > WAIT_NS) {
         *abort_flag = 1;
@@ -866,19 +916,27 @@ __device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned target,
         break;
       }
     }
-    __threadfence();
+    __threadfence();  // acquires what the other CTAs released
   }
   __syncthreads();
-  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
   return *abort_flag == 0;
 }
 
-// One product's tiles: `size` CTAs of the cluster share each tile's K (1: each CTA a tile). it: K atoms that this
-// CTA's ring has carried; tiles: tiles it has finished (the parity of tfull).
+// Where 16-byte chunk c of a row lies in a block of shares of `share` columns (16, 32 or 64): rows a thread each,
+// eight of them in eight different bank groups.
+__device__ __forceinline__ uint32_t share_at(int row, int c, int share) {
+  const int f = share == 16 ? (row >> 1) & 3 : row & 7;
+  return static_cast<uint32_t>(row * share * 4 + ((c ^ f) << 4));
+}
+
+// One product's tiles: `size` CTAs of the cluster share each tile's K (1: each CTA a tile). The CTAs of a split tile
+// send each other their shares of the columns that the other finishes, in bulk copies between shared memories.
+// it: K atoms that this CTA's ring has carried; tiles, splits: (split) tiles that it has finished.
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUtensorMap* tmB, const NsArgs& ep, int size,
-                                              const TileSmem& sm, uint32_t& it, uint32_t& tiles, int32_t* err) {
-  constexpr int STAGES = ATOMS;
+                                              const TileSmem& sm, uint32_t& it, uint32_t& tiles, uint32_t& splits, int32_t* err) {
+  constexpr int STAGES = FUSED_ATOMS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = size > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int num_m = (ep.M + 127) / 128, num_n = (ep.N + 127) / 128;
@@ -887,77 +945,126 @@ __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUte
   const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * rank / size);
   const int nk = static_cast<int>(static_cast<int64_t>(atoms) * (rank + 1) / size) - kb0;
   const int in_tile = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
-  const int share16 = 8 / size, count = share16 >= 2 ? share16 / 2 : (half == 0 ? share16 : 0);
-  for (int t = static_cast<int>(blockIdx.x) / size; t < num_tiles; t += static_cast<int>(gridDim.x) / size) {
+  const int share = 128 / size, count = share >= 32 ? share / 32 : (half == 0 ? 1 : 0);
+  const int step = static_cast<int>(gridDim.x) / size;
+  for (int t = static_cast<int>(blockIdx.x) / size; t < num_tiles; t += step) {
     int mb, nb;
     ns_tile(ep, t, num_m, num_n, mb, nb);
-    const int first_col = nb * 128 + rank * (128 / size) + half * count * 16, row = mb * 128 + in_tile;
-    const bool mirror = ep.sym && mb != nb;
-    Addend add[4];
-    bool done = true;
+    const int first_col = nb * 128 + rank * share + half * count * 16, row = mb * 128 + in_tile;
+    const bool mirror = ep.sym && mb != nb, diag = ep.sym && mb == nb;  // on the diagonal both operands are the same rows
     if (warp == 0) {
-      const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
-      for (int i = 0; i < nk; ++i) {
-        const uint32_t g = it + i, s = g % STAGES;
-        if (!warp_wait(smem_u32(&sm.empty[s]), ((g / STAGES) & 1u) ^ 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
-        if (lane == 0) {
+      if (lane == 0) {
+        const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + (diag ? 0 : rows_bytes(B_MN, nb * 128, ep.N));
+        for (int i = 0; i < nk; ++i) {
+          const uint32_t g = it + i, s = g % STAGES;
+          if (!wait_one(smem_u32(&sm.empty[s]), ((g / STAGES) & 1u) ^ 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
           const uint32_t fb = smem_u32(&sm.full[s]);
           mbar_expect_tx(fb, bytes);
           load_atom<A_MN>(smem_u32(sm.sA + s * HALF), MN_BOX, mb * 128, ep.M, (kb0 + i) * 64,
                           [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmA, fb, c0, c1); });
-          load_atom<B_MN>(smem_u32(sm.sB + s * HALF), MN_BOX, nb * 128, ep.N, (kb0 + i) * 64,
-                          [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmB, fb, c0, c1); });
+          if (!diag)
+            load_atom<B_MN>(smem_u32(sm.sB + s * HALF), MN_BOX, nb * 128, ep.N, (kb0 + i) * 64,
+                            [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmB, fb, c0, c1); });
         }
-        __syncwarp();
       }
+      __syncwarp();
     } else if (warp == 1) {
-      constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
-      bool ok = true;
-      for (int i = 0; i < nk; ++i) {
-        const uint32_t g = it + i, s = g % STAGES;
-        if (!warp_wait(smem_u32(&sm.full[s]), (g / STAGES) & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        if (lane == 0) {
-          const uint32_t a_base = smem_u32(sm.sA + s * HALF), b_base = smem_u32(sm.sB + s * HALF);
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16(128, 128, A_MN, B_MN);
+        const uint64_t a_desc = stage_desc<A_MN, 1>(smem_u32(sm.sA)), b_desc = stage_desc<B_MN, 1>(smem_u32(diag ? sm.sA : sm.sB));
+        bool ok = true;
+        for (int i = 0; i < nk; ++i) {
+          const uint32_t g = it + i, s = g % STAGES;
+          if (!wait_one(smem_u32(&sm.full[s]), (g / STAGES) & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint64_t ad = a_desc + s * (HALF >> 4), bd = b_desc + s * (HALF >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(sm.tmem, step_desc<A_MN, 1>(a_base, kk), step_desc<B_MN, 1>(b_base, kk), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16(sm.tmem, ad + step_off<A_MN>(kk), bd + step_off<B_MN>(kk), idesc, (i > 0 || kk > 0) ? 1u : 0u);
           umma_commit(smem_u32(&sm.empty[s]));
         }
-        __syncwarp();
+        if (ok) umma_commit(smem_u32(sm.tfull));
       }
-      if (ok && lane == 0) umma_commit(smem_u32(sm.tfull));
       __syncwarp();
     } else {
+      uint16_t* stage = reinterpret_cast<uint16_t*>(sm.recv + (warp - 2) * STAGE_BYTES);  // products with a result take no shares
+      Addend add[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (c < count) load_addend(ep, row, first_col + 16 * c, add[c]);
-      done = warp_wait(smem_u32(sm.tfull), tiles & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
+      bool done = warp_wait(smem_u32(sm.tfull), tiles & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
       fence_after();
-      if (done) {
-        const uint32_t tbase = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
+      const uint32_t tbase = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
+      if (size == 1) {
+        if (done) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
-          if (size == 1) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int col0 = first_col + c * 32 + 16 * h;
               float v[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
-              if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror);
+              if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror, stage);
             }
-          } else {
-            float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(sm.sA) + in_tile * RED_LD + half * 64 + c * 32);
+          }
+        }
+      } else {
+        // every product that read the ring has completed: the shares may overlay it, a block of 128 x share for each CTA
+        if (done) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              p[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
-                                 __uint_as_float(r[4 * i + 3]));
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int col = half * 64 + c * 32 + 4 * i, to = col / share;
+              *reinterpret_cast<float4*>(sm.sA + to * (128 * 4) * share + share_at(in_tile, (col - to * share) / 4, share)) =
+                  make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                              __uint_as_float(r[4 * i + 3]));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (warp == 2 && lane < size) {
+          if (lane == 0) mbar_expect_tx(smem_u32(sm.rfull), SHARES);
+          const uint32_t block = 128 * 4 * share, to = static_cast<uint32_t>(lane);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  map_to_rank(smem_u32(sm.recv) + rank * block, to)),
+              "r"(smem_u32(sm.sA) + to * block), "r"(block), "r"(map_to_rank(smem_u32(sm.rfull), to))
+              : "memory");
+        }
+        __syncwarp();
+        done = warp_wait(smem_u32(sm.rfull), splits & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE) && done;
+        if (done) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col0 = first_col + 16 * c;
+            if (c < count && col0 < ep.N) {
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0.f;
+              const int chunk = (half * count + c) * 4;
+              for (int p = 0; p < size; ++p) {
+                const uint8_t* from = sm.recv + p * (128 * 4) * share;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 f = *reinterpret_cast<const float4*>(from + share_at(in_tile, chunk + i, share));
+                  v[4 * i] += f.x;
+                  v[4 * i + 1] += f.y;
+                  v[4 * i + 2] += f.z;
+                  v[4 * i + 3] += f.w;
+                }
+              }
+              finish16(ep, row, col0, v, add[c], mirror, stage);
+            }
           }
         }
       }
@@ -965,48 +1072,11 @@ __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUte
     it += static_cast<uint32_t>(nk);
     ++tiles;
     fence_before();
-    if (size > 1) {
-      cluster_sync();  // the cluster's tiles are in shared memory
-      if (warp >= 2 && done) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col0 = first_col + 16 * c;
-          if (c < count && col0 < ep.N) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.f;
-            const uint32_t at = smem_u32(sm.sA) + (in_tile * RED_LD + (col0 - nb * 128)) * 4;
-            for (int p = 0; p < size; p += 2) {
-              float4 f[2][4];
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t from = map_to_rank(at, static_cast<uint32_t>(p + q));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                               : "=f"(f[q][i].x), "=f"(f[q][i].y), "=f"(f[q][i].z), "=f"(f[q][i].w)
-                               : "r"(from + 16 * i)
-                               : "memory");
-              }
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  v[4 * i] += f[q][i].x;
-                  v[4 * i + 1] += f[q][i].y;
-                  v[4 * i + 2] += f[q][i].z;
-                  v[4 * i + 3] += f[q][i].w;
-                }
-            }
-            finish16(ep, row, col0, v, add[c], mirror);
-          }
-        }
-      }
-      fence_proxy_async_smem();  // the ring takes tensor copies again where the tile was
-      cluster_sync();
-    } else {
+    if (size > 1) ++splits;
+    if (size > 1 && t + step < num_tiles)
+      cluster_sync();  // the peers have what they were sent, and have read what they received
+    else
       __syncthreads();  // the accumulator is read
-    }
     fence_after();
   }
 }
@@ -1018,19 +1088,22 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSmem sm;
   sm.sA = smem;
-  sm.sB = smem + ATOMS * HALF;
-  sm.full = reinterpret_cast<uint64_t*>(smem + RING);
-  sm.empty = sm.full + ATOMS;
-  sm.tfull = sm.empty + ATOMS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.tfull + 1);
+  sm.sB = smem + FUSED_ATOMS * HALF;
+  sm.recv = smem + FUSED_RING;
+  sm.full = reinterpret_cast<uint64_t*>(smem + FUSED_RING + SHARES);
+  sm.empty = sm.full + FUSED_ATOMS;
+  sm.tfull = sm.empty + FUSED_ATOMS;
+  sm.rfull = sm.tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.rfull + 1);
   sm.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ATOMS; ++s) {
+    for (int s = 0; s < FUSED_ATOMS; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     mbar_init(smem_u32(sm.tfull), 1);
+    mbar_init(smem_u32(sm.rfull), 1);
     *sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1047,31 +1120,31 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     scale_pass<4>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
   else
     scale_pass<1>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
-  uint32_t it = 0, tiles = 0;
+  uint32_t it = 0, tiles = 0, splits = 0;
   unsigned target = gridDim.x;
   bool ok = grid_barrier(a.counter, target, sm.abort_flag, err);
   for (int s = 0; s < a.steps && ok; ++s) {
     const __half* x = a.hi[s & 1];
     const bool fold = s >= a.two_term, last = s + 1 == a.steps;
     NsArgs e = gram_args(a.m, a.n, a.A, a.ld_a);
-    fused_product<TALL, TALL>(&maps.x_short[s & 1], &maps.x_short[s & 1], e, a.split, sm, it, tiles, err);
+    fused_product<TALL, TALL>(&maps.x_short[s & 1], &maps.x_short[s & 1], e, a.split, sm, it, tiles, splits, err);
     ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
     if (!ok) break;
     e = poly_args(a.m, a.A, a.P, a.ld_a, fold);
-    fused_product<false, false>(&maps.A, &maps.A, e, 1, sm, it, tiles, err);
+    fused_product<false, false>(&maps.A, &maps.A, e, 1, sm, it, tiles, splits, err);
     ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
     if (!ok) break;
     e = apply_args(a.m, a.n, TALL, fold, last, a.scale, x, a.lo, a.hi[(s + 1) & 1], s + 1 < a.two_term ? a.lo : nullptr, a.ld_x,
                    a.o, a.ld_o, a.bf_v16);
     if (TALL)
-      fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, sm, it, tiles, err);
+      fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, sm, it, tiles, splits, err);
     else
-      fused_product<false, true>(&maps.P, &maps.x_long[s & 1], e, 1, sm, it, tiles, err);
+      fused_product<false, true>(&maps.P, &maps.x_long[s & 1], e, 1, sm, it, tiles, splits, err);
     if (!last) ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
   }
   fence_before();
   __syncthreads();
-  if (cluster_size() > 1) cluster_sync();
+  if (cluster_size() > 1) cluster_sync();  // no CTA leaves while a peer may still send to it
   fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(sm.tmem) : "memory");
 }
@@ -1132,14 +1205,6 @@ bool pick_fused(int m, int n) {
   return tm * tn <= num_sms() && tm * (tm + 1) / 2 <= num_sms();
 }
 
-// CTAs that share K of a Gram product in the fused kernel (its cluster size).
-int fused_split(int m, int n) {
-  const int tm = (m + 127) / 128, tiles = tm * (tm + 1) / 2, atoms = (n + 63) / 64;
-  int split = 1;
-  while (split < 4 && tiles * split * 2 <= num_sms() && atoms >= split * 16) split *= 2;
-  return split;
-}
-
 // ------------------------------------------------------------------ short side of at most 64
 // u of the element k on the long side, i on the short one.
 struct TinyArgs {
@@ -1159,8 +1224,9 @@ struct TinyArgs {
 
 constexpr int CHUNK = 64;  // long-side elements a CTA holds at a time
 
-// u[k][i] of a chunk from k0 into shared memory (rows of 65); first: also writes m'.
-__device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, float (*u)[TINY + 1], bool first) {
+// u[k][i] of a chunk from k0 into shared memory; first: also writes m'.
+template <class T, int LD>
+__device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)[LD], bool first) {
   const int kn = static_cast<int>(min(static_cast<int64_t>(CHUNK), a.n - k0));
   for (int e = threadIdx.x; e < CHUNK * TINY; e += 256) {
     const int k = a.tall ? e / TINY : e % CHUNK, i = a.tall ? e % TINY : e / CHUNK;  // global memory's order
@@ -1179,29 +1245,27 @@ __device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, float 
         }
       }
     }
-    u[k][i] = v;
+    u[k][i] = static_cast<T>(v);
   }
 }
 
 // Partial Gram matrices u u^T in fp64, 4 x 4 of them a thread.
 __global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
-  __shared__ float u[CHUNK][TINY + 1];
+  __shared__ double u[CHUNK][TINY];
   release_next();
   double acc[4][4] = {};
   const int ti = threadIdx.x & 15, tj = threadIdx.x >> 4;
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk(a, c * CHUNK, u, true);
+    tiny_chunk<double, TINY>(a, c * CHUNK, u, true);
     __syncthreads();
     if (ti * 4 < a.m && tj * 4 < a.m) {
+#pragma unroll 4
       for (int k = 0; k < CHUNK; ++k) {
-        double x[4], y[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          x[q] = u[k][ti * 4 + q];
-          y[q] = u[k][tj * 4 + q];
-        }
+        const double2 x0 = *reinterpret_cast<const double2*>(&u[k][ti * 4]), x1 = *reinterpret_cast<const double2*>(&u[k][ti * 4 + 2]);
+        const double2 y0 = *reinterpret_cast<const double2*>(&u[k][tj * 4]), y1 = *reinterpret_cast<const double2*>(&u[k][tj * 4 + 2]);
+        const double x[4] = {x0.x, x0.y, x1.x, x1.y}, y[4] = {y0.x, y0.y, y1.x, y1.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1219,76 +1283,99 @@ __global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
     }
 }
 
-// c = sa * a b + sd * I, 64 x 64 matrices with rows of 65, 2 x 2 elements a thread of 1024 (32 x 32).
-__device__ __forceinline__ void mul64(float (*c)[TINY + 1], float (*a)[TINY + 1], float (*b)[TINY + 1], float sa, int m) {
-  const int i = (threadIdx.x >> 5) * 2, j = threadIdx.x & 31;
-  float s[2][2] = {};
-  if (i < m) {
-    for (int k = 0; k < m; ++k) {
-      const float x0 = a[i][k], x1 = a[i + 1][k], y0 = b[k][j], y1 = b[k][j + 32];
-      s[0][0] = fmaf(x0, y0, s[0][0]);
-      s[0][1] = fmaf(x0, y1, s[0][1]);
-      s[1][0] = fmaf(x1, y0, s[1][0]);
-      s[1][1] = fmaf(x1, y1, s[1][1]);
+// Their sum, into the first: 32 elements a block, 8 threads an element, each every eighth part.
+__global__ void __launch_bounds__(256) muon_tiny_reduce_kernel(TinyArgs a) {
+  __shared__ double red[8][32];
+  release_next();
+  wait_for_last();
+  const int mm = a.m * a.m, lane = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  double v = 0.0;
+  if (e < mm) {
+#pragma unroll 4
+    for (int p = y; p < a.parts; p += 8) v += a.gram[static_cast<int64_t>(p) * mm + e];
+  }
+  red[y][lane] = v;
+  __syncthreads();
+  if (y == 0 && e < mm) {
+    for (int k = 1; k < 8; ++k) v += red[k][lane];
+    a.gram[e] = v;  // the element's own part is read only by this block
+  }
+}
+
+using Mat64 = float (*)[TINY];
+
+// c = s * a b, 64 x 64. 1024 threads: four groups take a quarter of k each, 4 x 4 elements a thread, and their sums
+// meet in `part`. c may be a or b. (a and b are symmetric but for rounding; reading a by columns instead would let
+// that difference grow from step to step.)
+__device__ __forceinline__ void mul64(Mat64 c, Mat64 a, Mat64 b, float s, float4 (*part)[TINY * TINY / 4]) {
+  const int q = threadIdx.x >> 8, ti = threadIdx.x & 15, tj = (threadIdx.x >> 4) & 15;
+  float acc[4][4] = {};
+#pragma unroll
+  for (int k = q * 16; k < q * 16 + 16; k += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = *reinterpret_cast<const float4*>(&a[tj * 4 + i][k]);
+      y[i] = *reinterpret_cast<const float4*>(&b[k + i][ti * 4]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int l = 0; l < 4; ++l) {
+        acc[i][0] = fmaf(xs[l], y[l].x, acc[i][0]);
+        acc[i][1] = fmaf(xs[l], y[l].y, acc[i][1]);
+        acc[i][2] = fmaf(xs[l], y[l].z, acc[i][2]);
+        acc[i][3] = fmaf(xs[l], y[l].w, acc[i][3]);
+      }
     }
   }
-  __syncthreads();  // c may be a or b
-  c[i][j] = sa * s[0][0];
-  c[i][j + 32] = sa * s[0][1];
-  c[i + 1][j] = sa * s[1][0];
-  c[i + 1][j + 32] = sa * s[1][1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[q][(tj * 4 + i) * 16 + ti] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  __syncthreads();
+  const float4 p0 = part[0][threadIdx.x], p1 = part[1][threadIdx.x], p2 = part[2][threadIdx.x], p3 = part[3][threadIdx.x];
+  *reinterpret_cast<float4*>(&c[threadIdx.x >> 4][(threadIdx.x & 15) * 4]) =
+      make_float4(s * (p0.x + p1.x + (p2.x + p3.x)), s * (p0.y + p1.y + (p2.y + p3.y)), s * (p0.z + p1.z + (p2.z + p3.z)),
+                  s * (p0.w + p1.w + (p2.w + p3.w)));
   __syncthreads();
 }
 
-// The steps on the Gram matrix: with P = a I + b A + c A^2, Q <- P Q, A <- P A P. r = scale * Q / (|u| + eps).
+constexpr int TINY_SMEM = (4 + 4) * TINY * TINY * 4;
+
+// The steps on the Gram matrix: with P = a I + b A + c A^2, Q <- P Q, A <- A P^2. r = scale * Q / (|u| + eps).
 __global__ void __launch_bounds__(1024) muon_tiny_steps_kernel(TinyArgs a) {
-  extern __shared__ float tiny_smem[];
-  float(*A)[TINY + 1] = reinterpret_cast<float(*)[TINY + 1]>(tiny_smem);
-  float(*P)[TINY + 1] = A + TINY;
-  float(*Q)[TINY + 1] = P + TINY;
+  extern __shared__ __align__(16) float tiny_smem[];
+  Mat64 A = reinterpret_cast<Mat64>(tiny_smem), P = A + TINY, Q = P + TINY, P2 = Q + TINY;
+  float4(*part)[TINY * TINY / 4] = reinterpret_cast<float4(*)[TINY * TINY / 4]>(P2 + TINY);
   __shared__ double trace[TINY];
   release_next();
   wait_for_last();
-  const int mm = a.m * a.m;
-  double own[4];  // at most 4 elements of the Gram matrix a thread
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = threadIdx.x + q * 1024;
-    double s = 0.0;
-    if (e < mm)
-      for (int p = 0; p < a.parts; ++p) s += a.gram[static_cast<int64_t>(p) * mm + e];
-    own[q] = s;
-    if (e < mm && e / a.m == e % a.m) trace[e / a.m] = s;
-  }
-  for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
-    A[e / TINY][e % TINY] = 0.f;
-    Q[e / TINY][e % TINY] = e / TINY == e % TINY ? 1.f : 0.f;
-  }
+  if (threadIdx.x < TINY) trace[threadIdx.x] = static_cast<int>(threadIdx.x) < a.m ? a.gram[threadIdx.x * (a.m + 1)] : 0.0;
   __syncthreads();
   double sum = 0.0;
   for (int i = 0; i < a.m; ++i) sum += trace[i];
   const double norm = sqrt(sum) + a.eps;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = threadIdx.x + q * 1024;
-    if (e < mm) A[e / a.m][e % a.m] = static_cast<float>(own[q] / norm / norm);
+  for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
+    const int i = e / TINY, j = e % TINY;
+    A[i][j] = i < a.m && j < a.m ? static_cast<float>(a.gram[i * a.m + j] / norm / norm) : 0.f;
+    Q[i][j] = i == j ? 1.f : 0.f;
   }
   __syncthreads();
   for (int st = 0; st < a.steps; ++st) {
-    mul64(P, A, A, NS_C, a.m);
+    mul64(P, A, A, NS_C, part);
     for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
       const int i = e / TINY, j = e % TINY;
       P[i][j] += NS_B * A[i][j] + (i == j ? NS_A : 0.f);
     }
     __syncthreads();
-    mul64(Q, P, Q, 1.f, a.m);
+    mul64(Q, P, Q, 1.f, part);
     if (st + 1 < a.steps) {
-      mul64(A, P, A, 1.f, a.m);
-      mul64(A, A, P, 1.f, a.m);
+      mul64(P2, P, P, 1.f, part);
+      mul64(A, A, P2, 1.f, part);
     }
   }
   const double f = static_cast<double>(a.scale) / norm;
-  for (int e = threadIdx.x; e < mm; e += 1024) a.r[e] = static_cast<float>(Q[e / a.m][e % a.m] * f);
+  for (int e = threadIdx.x; e < a.m * a.m; e += 1024) a.r[e] = static_cast<float>(Q[e / a.m][e % a.m] * f);
 }
 
 // o = r u, a chunk of the long side a CTA.
@@ -1306,7 +1393,7 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   const int fast = threadIdx.x & 63, slow = threadIdx.x >> 6;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk(a, c * CHUNK, u, false);
+    tiny_chunk<float, TINY + 1>(a, c * CHUNK, u, false);
     __syncthreads();
     float s[16] = {};
     for (int j = 0; j < a.m; ++j) {
@@ -1368,10 +1455,8 @@ Walk make_walk(int64_t rows, int64_t cols, int vec) {
   while (w.tx_log2 > 0 && (int64_t(1) << (w.tx_log2 - 1)) * vec >= cols) --w.tx_log2;
   const int64_t width = (int64_t(1) << w.tx_log2) * vec, ty = 256 >> w.tx_log2;
   w.col_tiles = (cols + width - 1) / width;
-  for (w.reps = 8;; w.reps /= 2) {
-    w.tiles = w.col_tiles * ((rows + ty * w.reps - 1) / (ty * w.reps));
-    if (w.reps == 1 || w.tiles >= NORM_PARTS) return w;
-  }
+  w.tiles = w.col_tiles * ((rows + ty * REPS - 1) / (ty * REPS));
+  return w;
 }
 
 mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
@@ -1392,51 +1477,71 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
   MT_TRY(launch_check("muon_tiny_gram_kernel"));
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel)));
-  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", 1, 1024, 3 * TINY * (TINY + 1) * 4, 0, st, a));
+  MT_TRY(launch_ahead(muon_tiny_reduce_kernel, "muon_tiny_reduce_kernel", (a.m * a.m + 31) / 32, 256, 0, 0, st, a));
+  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", 1, 1024, TINY_SMEM, 0, st, a));
   const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
   return launch_ahead(muon_tiny_apply_kernel, "muon_tiny_apply_kernel", static_cast<int>(std::min<int64_t>(chunks, 4 * num_sms())),
                       256, 0, 0, st, a);
 }
 
+// Clusters of `split` CTAs that are resident at once (they lie within a GPC: fewer than SMs suggest); asked once a device.
 template <bool TALL>
-mt_status fused_launch(const FusedMaps& maps, const FusedArgs& a, cudaStream_t st) {
+mt_status fused_clusters(cudaLaunchConfig_t cfg, int split, int* out) {
+  static std::atomic<int> cache[64][3];
+  int dev = 0, most = 0;
+  MT_CUDA(cudaGetDevice(&dev));
+  std::atomic<int>* known = dev < 64 ? &cache[dev][split == 2 ? 0 : split == 4 ? 1 : 2] : nullptr;
+  if (known) most = known->load(std::memory_order_relaxed);
+  if (most == 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / split * split), 1, 1);
+    MT_CUDA(cudaOccupancyMaxActiveClusters(&most, ns_fused_kernel<TALL>, &cfg));
+    if (known && most > 0) known->store(most, std::memory_order_relaxed);
+  }
+  *out = most;
+  return MT_OK;
+}
+
+template <bool TALL>
+mt_status fused_launch(const FusedMaps& maps, FusedArgs a, cudaStream_t st) {
   int32_t* err = device_error_word();
   if (!err) return fail(MT_ERR_CUDA, "device error word unavailable");
   static SmemOptIn opt;
-  MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_fused_kernel<TALL>)));
-  // a CTA for each tile of the largest product, whole clusters, all resident
-  const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128;
-  const int want = std::max(tm * tn, tm * (tm + 1) / 2 * a.split);
+  MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_fused_kernel<TALL>), FUSED_SMEM));
+  // every CTA resident: one an SM. The Gram products, whose K is the long side, are split over the largest cluster
+  // (up to 8) that leaves each CTA four K atoms and the grid a CTA for each tile of the other products; sending the
+  // shares costs about 2 us, a K atom 0.3 us.
+  const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128, gram = tm * (tm + 1) / 2, atoms = (a.n + 63) / 64;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min((want + a.split - 1) / a.split, num_sms() / a.split) * a.split), 1, 1);
   cfg.blockDim = dim3(TILE_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = FUSED_SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
+  attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (a.split > 1) {
-    // clusters lie within a GPC: fewer of them may be resident at once than SMs suggest (asked once a device)
-    static std::atomic<int> cache[64][2];
-    int dev = 0, most = 0;
-    MT_CUDA(cudaGetDevice(&dev));
-    std::atomic<int>* known = dev < 64 ? &cache[dev][a.split == 2 ? 0 : 1] : nullptr;
-    if (known) most = known->load(std::memory_order_relaxed);
-    if (most == 0) {
-      cudaLaunchConfig_t full = cfg;
-      full.gridDim.x = static_cast<unsigned>(num_sms() / a.split * a.split);
-      MT_CUDA(cudaOccupancyMaxActiveClusters(&most, ns_fused_kernel<TALL>, &full));
-      if (most < 1) return fail(MT_ERR_CUDA, "ns_fused_kernel: no cluster of %d fits the device", a.split);
-      if (known) known->store(most, std::memory_order_relaxed);
+  a.split = 1;
+  int grid = num_sms();
+  for (int split = 8; split > 1; split /= 2) {
+    if (atoms < split * 4) continue;
+    int clusters = 0;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    MT_TRY(fused_clusters<TALL>(cfg, split, &clusters));
+    if (clusters >= gram && clusters * split >= tm * tn) {
+      a.split = split;
+      grid = clusters * split;
+      break;
     }
-    cfg.gridDim.x = std::min<unsigned>(cfg.gridDim.x, static_cast<unsigned>(most * a.split));
   }
+  attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
+  // no more of them than the largest product, or the scaling, has work for
+  const int64_t want = std::max<int64_t>(std::max<int64_t>(tm * tn, gram * a.split), std::min<int64_t>(a.walk.tiles, num_sms()));
+  grid = static_cast<int>(std::min<int64_t>(grid, (want + a.split - 1) / a.split * a.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   MT_CUDA(cudaLaunchKernelEx(&cfg, ns_fused_kernel<TALL>, maps, a, err));
   return launch_check("ns_fused_kernel");
 }
@@ -1482,7 +1587,7 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
     a.tall = tall;
     a.steps = c.steps;
     a.two_term = two_term;
-    a.split = fused_split(m, n);
+    a.split = 1;
     a.hi[0] = p.hi[0];
     a.hi[1] = p.hi[1];
     a.lo = p.lo;
