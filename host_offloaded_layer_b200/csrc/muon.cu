@@ -22,7 +22,7 @@
 // |u|_F is summed in fp64, so that no magnitude of g that fp32 holds over- or underflows.
 //
 // Matrices whose short side is at most 64 take no tensor cores: their Gram matrix (in fp64) is all that the
-// steps need, one CTA runs them on it in fp32, and the result is one product with u: four launches.
+// steps need, one cluster runs them on it in fp32, and the result is one product with u: four launches.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -1224,25 +1224,35 @@ struct TinyArgs {
 
 constexpr int CHUNK = 64;  // long-side elements a CTA holds at a time
 
-// u[k][i] of a chunk from k0 into shared memory; first: also writes m'.
+// u[k][i] of a chunk from k0 into shared memory; first: also writes m'. A thread's 16 elements are in flight together.
 template <class T, int LD>
 __device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)[LD], bool first) {
+  constexpr int N = CHUNK * TINY / 256;
   const int kn = static_cast<int>(min(static_cast<int64_t>(CHUNK), a.n - k0));
-  for (int e = threadIdx.x; e < CHUNK * TINY; e += 256) {
-    const int k = a.tall ? e / TINY : e % CHUNK, i = a.tall ? e % TINY : e / CHUNK;  // global memory's order
-    float v = 0.f;
-    if (k < kn && i < a.m) {
-      const int64_t row = a.tall ? k0 + k : i, col = a.tall ? i : k0 + k;
-      v = !a.p.m_in || first || a.p.nesterov ? a.p.g[row * a.p.ld_g + col] : 0.f;
-      if (a.p.m_in) {
-        const int64_t at = row * a.p.ld_m + col;
-        if (first) {
-          float mo;
-          v = momentum_step(a.p, v, a.p.m_in[at], mo);
-          a.p.m_out[at] = mo;
-        } else {
-          v = a.p.nesterov ? fmaf(a.p.mu, a.p.m_out[at], v) : a.p.m_out[at];
-        }
+  const bool want_g = !a.p.m_in || first || a.p.nesterov;
+  const float* m = first ? a.p.m_in : a.p.m_out;
+  float vg[N], vm[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int e = threadIdx.x + q * 256;  // global memory's order: along a row of the matrix
+    const int k = a.tall ? e / TINY : e % CHUNK, i = a.tall ? e % TINY : e / CHUNK;
+    const int64_t row = a.tall ? k0 + k : i, col = a.tall ? i : k0 + k;
+    const bool in = k < kn && i < a.m;
+    vg[q] = in && want_g ? a.p.g[row * a.p.ld_g + col] : 0.f;
+    vm[q] = in && a.p.m_in ? m[row * a.p.ld_m + col] : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int e = threadIdx.x + q * 256;
+    const int k = a.tall ? e / TINY : e % CHUNK, i = a.tall ? e % TINY : e / CHUNK;
+    float v = vg[q];
+    if (a.p.m_in) {
+      if (first) {
+        float mo;
+        v = momentum_step(a.p, v, vm[q], mo);
+        if (k < kn && i < a.m) a.p.m_out[(a.tall ? k0 + k : i) * a.p.ld_m + (a.tall ? i : k0 + k)] = mo;
+      } else {
+        v = a.p.nesterov ? fmaf(a.p.mu, vm[q], v) : vm[q];
       }
     }
     u[k][i] = static_cast<T>(v);
@@ -1303,23 +1313,24 @@ __global__ void __launch_bounds__(256) muon_tiny_reduce_kernel(TinyArgs a) {
 }
 
 using Mat64 = float (*)[TINY];
+constexpr int TINY_CTAS = 8, TINY_ROWS = TINY / TINY_CTAS;  // the steps' cluster, and the rows of each product that a CTA computes
 
-// c = s * a b, 64 x 64. 1024 threads: four groups take a quarter of k each, 4 x 4 elements a thread, and their sums
-// meet in `part`. c may be a or b. (a and b are symmetric but for rounding; reading a by columns instead would let
-// that difference grow from step to step.)
-__device__ __forceinline__ void mul64(Mat64 c, Mat64 a, Mat64 b, float s, float4 (*part)[TINY * TINY / 4]) {
-  const int q = threadIdx.x >> 8, ti = threadIdx.x & 15, tj = (threadIdx.x >> 4) & 15;
-  float acc[4][4] = {};
+// This CTA's rows of s * a b, 64 x 64 matrices that every CTA of the cluster holds whole: thread (q, r, c) sums a
+// quarter of k for 2 rows x 4 columns, the quarters meet in `part`, and thread t gets elements 2t, 2t + 1 of the
+// CTA's 8 x 64. (Operands are symmetric but for rounding; reading a by columns would let that difference grow from
+// step to step.)
+__device__ __forceinline__ float2 mul64(Mat64 a, Mat64 b, int rank, float (*part)[TINY_ROWS * TINY]) {
+  const int c = threadIdx.x & 15, r = (threadIdx.x >> 4) & 3, q = threadIdx.x >> 6, row = rank * TINY_ROWS + 2 * r;
+  float acc[2][4] = {};
 #pragma unroll
   for (int k = q * 16; k < q * 16 + 16; k += 4) {
-    float4 x[4], y[4];
+    float4 x[2], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = *reinterpret_cast<const float4*>(&a[tj * 4 + i][k]);
-      y[i] = *reinterpret_cast<const float4*>(&b[k + i][ti * 4]);
-    }
+    for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const float4*>(&a[row + i][k]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(&b[k + i][c * 4]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
       const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int l = 0; l < 4; ++l) {
@@ -1330,52 +1341,83 @@ __device__ __forceinline__ void mul64(Mat64 c, Mat64 a, Mat64 b, float s, float4
       }
     }
   }
+  __syncthreads();  // `part` of the product before is read
 #pragma unroll
-  for (int i = 0; i < 4; ++i) part[q][(tj * 4 + i) * 16 + ti] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float4*>(&part[q][(2 * r + i) * TINY + c * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   __syncthreads();
-  const float4 p0 = part[0][threadIdx.x], p1 = part[1][threadIdx.x], p2 = part[2][threadIdx.x], p3 = part[3][threadIdx.x];
-  *reinterpret_cast<float4*>(&c[threadIdx.x >> 4][(threadIdx.x & 15) * 4]) =
-      make_float4(s * (p0.x + p1.x + (p2.x + p3.x)), s * (p0.y + p1.y + (p2.y + p3.y)), s * (p0.z + p1.z + (p2.z + p3.z)),
-                  s * (p0.w + p1.w + (p2.w + p3.w)));
-  __syncthreads();
+  float2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float2*>(&part[i][2 * threadIdx.x]);
+  return make_float2(v[0].x + v[1].x + (v[2].x + v[3].x), v[0].y + v[1].y + (v[2].y + v[3].y));
 }
 
-constexpr int TINY_SMEM = (4 + 4) * TINY * TINY * 4;
+// Elements 2t, 2t + 1 of this CTA's rows of c, to every CTA of the cluster.
+__device__ __forceinline__ void share64(Mat64 c, int rank, float2 v) {
+  const uint32_t at = smem_u32(&c[rank * TINY_ROWS][0]) + threadIdx.x * 8;
+#pragma unroll
+  for (int p = 0; p < TINY_CTAS; ++p)
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_to_rank(at, static_cast<uint32_t>(p))), "f"(v.x), "f"(v.y)
+                 : "memory");
+}
 
-// The steps on the Gram matrix: with P = a I + b A + c A^2, Q <- P Q, A <- A P^2. r = scale * Q / (|u| + eps).
-__global__ void __launch_bounds__(1024) muon_tiny_steps_kernel(TinyArgs a) {
+constexpr int TINY_SMEM = (6 * TINY * TINY + 4 * TINY_ROWS * TINY) * 4;
+
+// The steps on the Gram matrix, eight CTAs of a cluster with eight rows each: with P = a I + b A + c A^2,
+// Q <- P Q, A <- A P^2. A product writes no matrix that it reads, and a cluster barrier stands behind each.
+// r = scale * Q / (|u| + eps).
+__global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_tiny_steps_kernel(TinyArgs a) {
   extern __shared__ __align__(16) float tiny_smem[];
-  Mat64 A = reinterpret_cast<Mat64>(tiny_smem), P = A + TINY, Q = P + TINY, P2 = Q + TINY;
-  float4(*part)[TINY * TINY / 4] = reinterpret_cast<float4(*)[TINY * TINY / 4]>(P2 + TINY);
+  Mat64 A = reinterpret_cast<Mat64>(tiny_smem), A_next = A + TINY, P = A + 2 * TINY, P2 = A + 3 * TINY, Q = A + 4 * TINY,
+        Q_next = A + 5 * TINY;
+  float(*part)[TINY_ROWS * TINY] = reinterpret_cast<float(*)[TINY_ROWS * TINY]>(A + 6 * TINY);
   __shared__ double trace[TINY];
+  const int rank = static_cast<int>(cluster_rank());
   release_next();
   wait_for_last();
   if (threadIdx.x < TINY) trace[threadIdx.x] = static_cast<int>(threadIdx.x) < a.m ? a.gram[threadIdx.x * (a.m + 1)] : 0.0;
+  double own[TINY * TINY / 256];
+#pragma unroll
+  for (int q = 0; q < TINY * TINY / 256; ++q) {
+    const int e = threadIdx.x + q * 256, i = e / TINY, j = e % TINY;
+    own[q] = i < a.m && j < a.m ? a.gram[i * a.m + j] : 0.0;
+  }
   __syncthreads();
   double sum = 0.0;
   for (int i = 0; i < a.m; ++i) sum += trace[i];
-  const double norm = sqrt(sum) + a.eps;
-  for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
-    const int i = e / TINY, j = e % TINY;
-    A[i][j] = i < a.m && j < a.m ? static_cast<float>(a.gram[i * a.m + j] / norm / norm) : 0.f;
-    Q[i][j] = i == j ? 1.f : 0.f;
+  const double norm = sqrt(sum) + a.eps, inv = 1.0 / norm;
+#pragma unroll
+  for (int q = 0; q < TINY * TINY / 256; ++q) {
+    const int e = threadIdx.x + q * 256;
+    A[e / TINY][e % TINY] = static_cast<float>(own[q] * inv * inv);
+    Q[e / TINY][e % TINY] = e / TINY == e % TINY ? 1.f : 0.f;
   }
-  __syncthreads();
+  cluster_sync();  // every CTA has started, and holds A
+  const int own_row = rank * TINY_ROWS + (threadIdx.x >> 5), own_col = 2 * (threadIdx.x & 31);
   for (int st = 0; st < a.steps; ++st) {
-    mul64(P, A, A, NS_C, part);
-    for (int e = threadIdx.x; e < TINY * TINY; e += 1024) {
-      const int i = e / TINY, j = e % TINY;
-      P[i][j] += NS_B * A[i][j] + (i == j ? NS_A : 0.f);
-    }
-    __syncthreads();
-    mul64(Q, P, Q, 1.f, part);
+    float2 v = mul64(A, A, rank, part);
+    v.x = fmaf(NS_C, v.x, fmaf(NS_B, A[own_row][own_col], own_row == own_col ? NS_A : 0.f));
+    v.y = fmaf(NS_C, v.y, fmaf(NS_B, A[own_row][own_col + 1], own_row == own_col + 1 ? NS_A : 0.f));
+    share64(P, rank, v);
+    cluster_sync();
+    share64(Q_next, rank, mul64(P, Q, rank, part));
     if (st + 1 < a.steps) {
-      mul64(P2, P, P, 1.f, part);
-      mul64(A, A, P2, 1.f, part);
+      share64(P2, rank, mul64(P, P, rank, part));
+      cluster_sync();
+      share64(A_next, rank, mul64(A, P2, rank, part));
     }
+    cluster_sync();
+    Mat64 t = Q;
+    Q = Q_next;
+    Q_next = t;
+    t = A;
+    A = A_next;
+    A_next = t;
   }
-  const double f = static_cast<double>(a.scale) / norm;
-  for (int e = threadIdx.x; e < a.m * a.m; e += 1024) a.r[e] = static_cast<float>(Q[e / a.m][e % a.m] * f);
+  const double f = a.scale * inv;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (own_row < a.m && own_col + q < a.m) a.r[own_row * a.m + own_col + q] = static_cast<float>(Q[own_row][own_col + q] * f);
 }
 
 // o = r u, a chunk of the long side a CTA.
@@ -1478,7 +1520,7 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel)));
   MT_TRY(launch_ahead(muon_tiny_reduce_kernel, "muon_tiny_reduce_kernel", (a.m * a.m + 31) / 32, 256, 0, 0, st, a));
-  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", 1, 1024, TINY_SMEM, 0, st, a));
+  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", TINY_CTAS, 256, TINY_SMEM, 0, st, a));
   const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
   return launch_ahead(muon_tiny_apply_kernel, "muon_tiny_apply_kernel", static_cast<int>(std::min<int64_t>(chunks, 4 * num_sms())),
                       256, 0, 0, st, a);
