@@ -1261,20 +1261,22 @@ __device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)
 
 // Partial Gram matrices u u^T in fp64, 4 x 4 of them a thread.
 __global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
-  __shared__ double u[CHUNK][TINY];
+  __shared__ __align__(16) double u[CHUNK][TINY + 2];
   release_next();
   double acc[4][4] = {};
+  // a thread's columns: pairs 32 apart, so that a warp reads whole rows without bank conflicts
   const int ti = threadIdx.x & 15, tj = threadIdx.x >> 4;
+  auto at = [](int t, int q) { return (q >> 1) * 32 + 2 * t + (q & 1); };
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk<double, TINY>(a, c * CHUNK, u, true);
+    tiny_chunk<double, TINY + 2>(a, c * CHUNK, u, true);
     __syncthreads();
-    if (ti * 4 < a.m && tj * 4 < a.m) {
+    if (2 * ti < a.m && 2 * tj < a.m) {
 #pragma unroll 4
       for (int k = 0; k < CHUNK; ++k) {
-        const double2 x0 = *reinterpret_cast<const double2*>(&u[k][ti * 4]), x1 = *reinterpret_cast<const double2*>(&u[k][ti * 4 + 2]);
-        const double2 y0 = *reinterpret_cast<const double2*>(&u[k][tj * 4]), y1 = *reinterpret_cast<const double2*>(&u[k][tj * 4 + 2]);
+        const double2 x0 = *reinterpret_cast<const double2*>(&u[k][2 * ti]), x1 = *reinterpret_cast<const double2*>(&u[k][2 * ti + 32]);
+        const double2 y0 = *reinterpret_cast<const double2*>(&u[k][2 * tj]), y1 = *reinterpret_cast<const double2*>(&u[k][2 * tj + 32]);
         const double x[4] = {x0.x, x0.y, x1.x, x1.y}, y[4] = {y0.x, y0.y, y1.x, y1.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1288,7 +1290,7 @@ __global__ void __launch_bounds__(256) muon_tiny_gram_kernel(TinyArgs a) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = ti * 4 + i, s = tj * 4 + j;
+      const int r = at(ti, i), s = at(tj, j);
       if (r < a.m && s < a.m) out[r * a.m + s] = acc[i][j];
     }
 }
@@ -1301,7 +1303,7 @@ __global__ void __launch_bounds__(256) muon_tiny_reduce_kernel(TinyArgs a) {
   const int mm = a.m * a.m, lane = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
   double v = 0.0;
   if (e < mm) {
-#pragma unroll 4
+#pragma unroll 10
     for (int p = y; p < a.parts; p += 8) v += a.gram[static_cast<int64_t>(p) * mm + e];
   }
   red[y][lane] = v;
@@ -1420,14 +1422,21 @@ __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_ti
     if (own_row < a.m && own_col + q < a.m) a.r[own_row * a.m + own_col + q] = static_cast<float>(Q[own_row][own_col + q] * f);
 }
 
-// o = r u, a chunk of the long side a CTA.
+// o = r u, a chunk of the long side a CTA. Rows of 68 in shared memory: four j a read, no bank conflicts.
+constexpr int APPLY_LD = TINY + 4;
 __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
-  __shared__ float u[CHUNK][TINY + 1];
-  __shared__ float r[TINY][TINY + 1];
+  __shared__ __align__(16) float u[CHUNK][APPLY_LD];
+  __shared__ __align__(16) float r[TINY][APPLY_LD];
   wait_for_last();
-  for (int e = threadIdx.x; e < TINY * TINY; e += 256) {
-    const int i = e / TINY, j = e % TINY;
-    r[i][j] = i < a.m && j < a.m ? a.r[i * a.m + j] : 0.f;
+  {
+    float v[TINY * TINY / 256];
+#pragma unroll
+    for (int q = 0; q < TINY * TINY / 256; ++q) {
+      const int i = (threadIdx.x + q * 256) / TINY, j = threadIdx.x % TINY;
+      v[q] = i < a.m && j < a.m ? a.r[i * a.m + j] : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < TINY * TINY / 256; ++q) r[(threadIdx.x + q * 256) / TINY][threadIdx.x % TINY] = v[q];
   }
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
   // neighbouring threads write neighbouring elements of a row of o: along the short side of a tall matrix, the long
@@ -1435,14 +1444,19 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   const int fast = threadIdx.x & 63, slow = threadIdx.x >> 6;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk<float, TINY + 1>(a, c * CHUNK, u, false);
+    tiny_chunk<float, APPLY_LD>(a, c * CHUNK, u, false);
     __syncthreads();
     float s[16] = {};
-    for (int j = 0; j < a.m; ++j) {
+    const float(*mine)[APPLY_LD] = a.tall ? r : u, (*other)[APPLY_LD] = a.tall ? u : r;
+    for (int j = 0; j < a.m; j += 4) {  // zeros behind a.m
+      const float4 x = *reinterpret_cast<const float4*>(&mine[fast][j]);
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        const int k = a.tall ? slow + 4 * q : fast, i = a.tall ? fast : slow + 4 * q;
-        s[q] = fmaf(r[i][j], u[k][j], s[q]);
+        const float4 y = *reinterpret_cast<const float4*>(&other[slow + 4 * q][j]);
+        s[q] = fmaf(x.x, y.x, s[q]);
+        s[q] = fmaf(x.y, y.y, s[q]);
+        s[q] = fmaf(x.z, y.z, s[q]);
+        s[q] = fmaf(x.w, y.w, s[q]);
       }
     }
 #pragma unroll
