@@ -219,14 +219,15 @@ __global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const d
 }
 
 // ------------------------------------------------------------------ products
-// v = alpha * (A B^T)[r, c] + beta * (add_hi + add_lo)[r, c] + diag (r == c), stored as fp16 (head, and rest
+// v = alpha * (A B^T)[r, c] + beta * add_hi[r, c] + beta_lo * add_lo[r, c] + diag (r == c), stored as fp16 (head, and rest
 // where out_lo is set) or, where out_bf is set, as bf16. Internal matrices have rows of whole 64-element
 // groups, so 16-column chunks are always stored whole there.
 struct NsArgs {
   int M, N, K;
   int sym;     // square and symmetric: tiles on and below the diagonal only, each stored twice
   int raster;  // 1: row blocks outer; 2: column blocks outer (the polynomial's matrix stays in L2)
-  float alpha, beta, diag;
+  int full_tiles;  // 256 x 256 tiles; the ones behind them are done in two halves of 128 columns
+  float alpha, beta, beta_lo, diag;
   const __half *add_hi, *add_lo;
   __half *out_hi, *out_lo;
   int64_t ld_add, ld_out;
@@ -247,33 +248,39 @@ __host__ __device__ __forceinline__ NsArgs gram_args(int m, int n, __half* A, in
   return e;
 }
 
-// P = b A + c A^2 (fold: + a I), times S_P.
-__host__ __device__ __forceinline__ NsArgs poly_args(int m, const __half* A, __half* P, int64_t ld_a, bool fold) {
+// A product of two m x m matrices that commute with each other (polynomials of A): symmetric.
+__host__ __device__ __forceinline__ NsArgs square_args(int m, int64_t ld_a, __half* out, float alpha) {
   NsArgs e = {};
   e.M = e.N = e.K = m;
   e.sym = 1;
-  e.alpha = NS_C * S_P / (S_A * S_A);
-  e.beta = NS_B * S_P / S_A;
-  e.diag = fold ? NS_A * S_P : 0.f;
-  e.add_hi = A;
-  e.ld_add = ld_a;
-  e.out_hi = P;
-  e.ld_out = ld_a;
+  e.alpha = alpha;
+  e.out_hi = out;
+  e.ld_add = e.ld_out = ld_a;
   return e;
 }
 
-// X' = P X (X P in a tall matrix), where P has no a on its diagonal + a X; the last one is the result.
-__host__ __device__ __forceinline__ NsArgs apply_args(int m, int n, bool tall, bool fold, bool last, float scale, const __half* x,
-                                                      const __half* lo, __half* out_hi, __half* out_lo, int64_t ld_x,
+// P = b A + c A^2 (fold: + a I), times S_P.
+__host__ __device__ __forceinline__ NsArgs poly_args(int m, const __half* A, __half* P, int64_t ld_a, bool fold) {
+  NsArgs e = square_args(m, ld_a, P, NS_C * S_P / (S_A * S_A));
+  e.beta = NS_B * S_P / S_A;
+  e.diag = fold ? NS_A * S_P : 0.f;
+  e.add_hi = A;
+  return e;
+}
+
+// X' = P X (X P in a tall matrix), P held times s_p, + lead * X where P lacks that multiple of I (lead = 0: it does
+// not); the last one is the result.
+__host__ __device__ __forceinline__ NsArgs apply_args(int m, int n, bool tall, float lead, float s_p, bool last, float scale,
+                                                      const __half* x, const __half* lo, __half* out_hi, __half* out_lo, int64_t ld_x,
                                                       __nv_bfloat16* o, int64_t ld_o, int bf_v16) {
   NsArgs e = {};
   e.M = tall ? n : m;
   e.N = tall ? m : n;
   e.K = m;
   e.raster = tall ? 1 : 2;
-  e.alpha = (last ? scale / S_X : 1.f) / S_P;
-  if (!fold) {
-    e.beta = NS_A;
+  e.alpha = (last ? scale / S_X : 1.f) / s_p;
+  if (lead != 0.f) {
+    e.beta = e.beta_lo = lead;
     e.add_hi = x;
     e.add_lo = lo;
     e.ld_add = ld_x;
@@ -343,8 +350,8 @@ __device__ __forceinline__ void finish16(const NsArgs& e, int row, int col0, flo
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 l = h2f(a.lo[i]);
-      v[2 * i] = fmaf(e.beta, l.x, v[2 * i]);
-      v[2 * i + 1] = fmaf(e.beta, l.y, v[2 * i + 1]);
+      v[2 * i] = fmaf(e.beta_lo, l.x, v[2 * i]);
+      v[2 * i + 1] = fmaf(e.beta_lo, l.y, v[2 * i + 1]);
     }
   }
   if (e.diag != 0.f) {
@@ -504,11 +511,12 @@ __device__ __forceinline__ constexpr uint64_t step_off(int kk) {
 // ---------------------------------------------------------------- 256 x 256 tiles on two SMs
 // A persistent cluster of two CTAs: each stages its 128 rows of A and 128 columns of B, the even one issues
 // cta_group::2 products for both into one of two 256-column accumulators, and both drain theirs while the
-// next tile runs.
+// next tile runs. A last wave that would leave half of the clusters idle or more is done in half tiles (256 x 128):
+// the 105 tiles of a symmetric 3584 x 3584 product take 74 clusters for 1.6 tiles' time instead of two.
 template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
-    ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsArgs ep,
-                   int32_t* err) {
+    ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmB64, const __grid_constant__ NsArgs ep, int32_t* err) {
   constexpr int KA = 2, STAGES = ATOMS / KA, OP_STAGE = HALF * KA, BK = 64 * KA;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -525,8 +533,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
   const int num_m = (ep.M + 255) / 256, num_n = (ep.N + 255) / 256;
-  const int num_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
+  const int all_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
+  const int num_tiles = ep.full_tiles + 2 * (all_tiles - ep.full_tiles);
   const int num_kb = (ep.K + BK - 1) / BK;
+  // tile t: its blocks, its first column, and whether it is half a tile
+  auto locate = [&](int t, int& mb, int& nb, int& n0) {
+    const int u = t - ep.full_tiles;
+    ns_tile(ep, u < 0 ? t : ep.full_tiles + u / 2, num_m, num_n, mb, nb);
+    n0 = nb * 256 + (u < 0 ? 0 : (u & 1) * 128);
+    return u >= 0;
+  };
 
   release_next();
   if (threadIdx.x == 0) {
@@ -556,9 +572,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int t = cluster; t < num_tiles && ok; t += n_clusters) {
-      int mb, nb;
-      ns_tile(ep, t, num_m, num_n, mb, nb);
-      const int m_own = mb * 256 + static_cast<int>(rank) * 128, n_own = nb * 256 + static_cast<int>(rank) * 128;
+      int mb, nb, n0;
+      const bool halved = locate(t, mb, nb, n0);
+      const int m_own = mb * 256 + static_cast<int>(rank) * 128, n_own = n0 + static_cast<int>(rank) * (halved ? 64 : 128);
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
         const int s = it % STAGES;
         if (!warp_wait(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) {
@@ -570,7 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           const int k0 = kb * BK, atoms = min(KA, (ep.K - k0 + 63) / 64);
           if (rank == 0) {
             const uint32_t bytes = rows_bytes(A_MN, mb * 256, ep.M) + rows_bytes(A_MN, mb * 256 + 128, ep.M) +
-                                   rows_bytes(B_MN, nb * 256, ep.N) + rows_bytes(B_MN, nb * 256 + 128, ep.N);
+                                   (halved ? (n0 < ep.N ? MN_BOX : 0) + (n0 + 64 < ep.N ? MN_BOX : 0)
+                                           : rows_bytes(B_MN, n0, ep.N) + rows_bytes(B_MN, n0 + 128, ep.N));
             mbar_expect_tx(smem_u32(&full[s]), bytes * static_cast<uint32_t>(atoms));
           }
           auto load = [&](const CUtensorMap* map) {
@@ -585,7 +602,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           const uint32_t a_dst = smem_u32(sA + s * OP_STAGE), b_dst = smem_u32(sB + s * OP_STAGE);
           for (int at = 0; at < atoms; ++at) {
             load_atom<A_MN>(a_dst + at * (A_MN ? MN_BOX : HALF), KA * MN_BOX, m_own, ep.M, k0 + 64 * at, load(&tmA));
-            load_atom<B_MN>(b_dst + at * (B_MN ? MN_BOX : HALF), KA * MN_BOX, n_own, ep.N, k0 + 64 * at, load(&tmB));
+            if (!halved) {
+              load_atom<B_MN>(b_dst + at * (B_MN ? MN_BOX : HALF), KA * MN_BOX, n_own, ep.N, k0 + 64 * at, load(&tmB));
+            } else if (n_own < ep.N) {  // 64 rows: one box in either order
+              if (B_MN)
+                load(&tmB64)(b_dst + at * MN_BOX, n_own, k0 + 64 * at);
+              else
+                load(&tmB64)(b_dst + at * HALF, k0 + 64 * at, n_own);
+            }
           }
         }
         __syncwarp();
@@ -593,7 +617,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_f16(256, 256, A_MN, B_MN);
       constexpr uint16_t both = 0x3;
       auto commit = [&](uint64_t* bar) {
         asm volatile(
@@ -607,6 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++tl) {
         const int ab = tl & 1;
+        const uint32_t idesc = t < ep.full_tiles ? idesc_f16(256, 256, A_MN, B_MN) : idesc_f16(256, 128, A_MN, B_MN);
         if (!warp_wait(smem_u32(&tempty[ab]), ((tl >> 1) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) break;
         fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(ab * 256);
@@ -642,14 +666,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int tl = 0;
     for (int t = cluster; t < num_tiles; t += n_clusters, ++tl) {
       const int ab = tl & 1;
-      int mb, nb;
-      ns_tile(ep, t, num_m, num_n, mb, nb);
+      int mb, nb, n0;
+      const bool halved = locate(t, mb, nb, n0);
       if (!warp_wait(smem_u32(&tfull[ab]), (tl >> 1) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE)) break;
       fence_after();
       const int row = mb * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * 256);
-      for (int c = 0; c < 8; ++c) {
-        const int col0 = nb * 256 + c * 32;
+      for (int c = 0; c < (halved ? 4 : 8); ++c) {
+        const int col0 = n0 + c * 32;
         if (col0 >= ep.N) break;
         Addend add[2];
         load_addend(ep, row, col0, add[0]);
@@ -1134,7 +1158,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     fused_product<false, false>(&maps.A, &maps.A, e, 1, sm, it, tiles, splits, err);
     ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
     if (!ok) break;
-    e = apply_args(a.m, a.n, TALL, fold, last, a.scale, x, a.lo, a.hi[(s + 1) & 1], s + 1 < a.two_term ? a.lo : nullptr, a.ld_x,
+    e = apply_args(a.m, a.n, TALL, fold ? 0.f : NS_A, S_P, last, a.scale, x, a.lo, a.hi[(s + 1) & 1], s + 1 < a.two_term ? a.lo : nullptr, a.ld_x,
                    a.o, a.ld_o, a.bf_v16);
     if (TALL)
       fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, sm, it, tiles, splits, err);
@@ -1157,22 +1181,37 @@ struct Operand {
   int64_t rows;
 };
 
-mt_status operand_map(CUtensorMap* m, const Operand& o, int64_t K) {
-  return o.mn ? tma_map_2d(m, o.p, o.rows, K, o.ld, 64, 64) : tma_map_2d(m, o.p, K, o.rows, o.ld, 64, 128);
+// Its tensor maps: boxes of 128 rows (MN-major: 64), and of 64.
+struct OperandMaps {
+  CUtensorMap rows128, rows64;
+  bool mn;
+};
+mt_status operand_maps(OperandMaps* m, const Operand& o, int64_t K) {
+  m->mn = o.mn;
+  if (o.mn) {
+    MT_TRY(tma_map_2d(&m->rows128, o.p, o.rows, K, o.ld, 64, 64));
+    m->rows64 = m->rows128;
+    return MT_OK;
+  }
+  MT_TRY(tma_map_2d(&m->rows128, o.p, K, o.rows, o.ld, 64, 128));
+  return tma_map_2d(&m->rows64, o.p, K, o.rows, o.ld, 64, 64);
 }
 
 // Clusters of two that run at once: one CTA an SM.
 int pair_clusters() { return std::max(1, num_sms() / 2); }
 
 template <bool A_MN, bool B_MN>
-mt_status ns_launch(const CUtensorMap& ta, const CUtensorMap& tb, const NsArgs& e, int split, cudaStream_t st) {
+mt_status ns_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tb64, NsArgs e, int split, cudaStream_t st) {
   int32_t* err = device_error_word();
   if (!err) return fail(MT_ERR_CUDA, "device error word unavailable");
   if (split == 0) {
     static SmemOptIn opt;
     MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_pair_kernel<A_MN, B_MN>)));
-    const int clusters = std::min(ns_tiles(e, 256), pair_clusters());
-    return launch_ahead(ns_pair_kernel<A_MN, B_MN>, "ns_pair_kernel", 2 * clusters, NS_THREADS, SMEM_BYTES, 0, st, ta, tb, e, err);
+    const int tiles = ns_tiles(e, 256), most = pair_clusters(), over = tiles % most;
+    e.full_tiles = 2 * over <= most ? tiles - over : tiles;
+    const int clusters = std::min(e.full_tiles + 2 * (tiles - e.full_tiles), most);
+    return launch_ahead(ns_pair_kernel<A_MN, B_MN>, "ns_pair_kernel", 2 * clusters, NS_THREADS, SMEM_BYTES, 0, st, ta, tb, tb64, e,
+                        err);
   }
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_tile_kernel<A_MN, B_MN>)));
@@ -1191,11 +1230,11 @@ int pick_split(const NsArgs& e) {
   return split;
 }
 
-mt_status ns_product(const CUtensorMap& ta, bool a_mn, const CUtensorMap& tb, bool b_mn, const NsArgs& e, cudaStream_t st) {
+mt_status ns_product(const OperandMaps& a, const OperandMaps& b, const NsArgs& e, cudaStream_t st) {
   const int split = pick_split(e);
-  if (!a_mn && !b_mn) return ns_launch<false, false>(ta, tb, e, split, st);
-  if (!a_mn) return ns_launch<false, true>(ta, tb, e, split, st);
-  return ns_launch<true, true>(ta, tb, e, split, st);
+  if (!a.mn && !b.mn) return ns_launch<false, false>(a.rows128, b.rows128, b.rows64, e, split, st);
+  if (!a.mn) return ns_launch<false, true>(a.rows128, b.rows128, b.rows64, e, split, st);
+  return ns_launch<true, true>(a.rows128, b.rows128, b.rows64, e, split, st);
 }
 
 // Whether all steps run as one kernel: each product's tiles fit the GPU about once, so that whole SM pairs on
@@ -1475,11 +1514,14 @@ struct Plan {
   int parts;
   double* part;
   unsigned* counter;
-  __half *hi[2], *lo, *A, *P;
+  __half *hi[2], *lo, *A, *P, *C;  // C: only where the first two steps share a Gram matrix
   double* gram;
   float* r;
   uint64_t bytes;
 };
+
+// Whether the first two steps of a matrix this wide share a Gram matrix: 3 m^2 n of products saved for 3 m^3 more.
+bool pair_first_steps(int64_t m, int64_t n) { return n >= 2 * m; }
 
 Plan plan(int64_t rows, int64_t cols, void* ws) {
   Plan p = {};
@@ -1500,6 +1542,7 @@ Plan plan(int64_t rows, int64_t cols, void* ws) {
     p.lo = b.take<__half>(rows * p.ld_x);
     p.A = b.take<__half>(p.m * p.ld_a);
     p.P = b.take<__half>(p.m * p.ld_a);
+    p.C = pair_first_steps(p.m, p.n) ? b.take<__half>(p.m * p.ld_a) : nullptr;
   }
   p.bytes = b.used;
   return p;
@@ -1615,22 +1658,26 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(o);
   const int bf_v16 = a16(o) && ld_o % 8 == 0;
   // X with the short or the long side as rows: K-major or MN-major by the matrix's orientation
-  FusedMaps maps;
+  OperandMaps x_short[2], x_long[2], sq_a, sq_p, sq_c;
   for (int i = 0; i < 2; ++i) {
-    MT_TRY(operand_map(&maps.x_short[i], Operand{p.hi[i], p.ld_x, tall, p.m}, n));
-    MT_TRY(operand_map(&maps.x_long[i], Operand{p.hi[i], p.ld_x, !tall, p.n}, m));
+    MT_TRY(operand_maps(&x_short[i], Operand{p.hi[i], p.ld_x, tall, p.m}, n));
+    MT_TRY(operand_maps(&x_long[i], Operand{p.hi[i], p.ld_x, !tall, p.n}, m));
   }
-  MT_TRY(operand_map(&maps.A, Operand{p.A, p.ld_a, false, p.m}, m));
-  MT_TRY(operand_map(&maps.P, Operand{p.P, p.ld_a, false, p.m}, m));
-  const double mm = static_cast<double>(m) * m;
-  add_exec_flops(2.0 * c.steps * (0.5 * mm * n + 0.5 * mm * m + mm * n));
-
+  MT_TRY(operand_maps(&sq_a, Operand{p.A, p.ld_a, false, p.m}, m));
+  MT_TRY(operand_maps(&sq_p, Operand{p.P, p.ld_a, false, p.m}, m));
   if (v4)
     muon_norm_kernel<4><<<parts, 256, 0, st>>>(g, w, p.part, p.counter);
   else
     muon_norm_kernel<1><<<parts, 256, 0, st>>>(g, w, p.part, p.counter);
   MT_TRY(launch_check("muon_norm_kernel"));
   if (pick_fused(m, n)) {
+    FusedMaps maps;
+    for (int i = 0; i < 2; ++i) {
+      maps.x_short[i] = x_short[i].rows128;
+      maps.x_long[i] = x_long[i].rows128;
+    }
+    maps.A = sq_a.rows128;
+    maps.P = sq_p.rows128;
     FusedArgs a;
     a.grad = g;
     a.walk = w;
@@ -1664,14 +1711,42 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
   else
     MT_TRY(launch_ahead(muon_scale_kernel<1>, "muon_scale_kernel", parts, 256, 0, 0, st, g, w, p.part, parts, c.eps, p.hi[0], lo,
                         p.ld_x));
-  for (int s = 0; s < c.steps; ++s) {
+  int s = 0;
+  if (p.C && two_term >= 2) {
+    // The first two steps on one Gram matrix: with P = b A + c A^2 the second step's is
+    // A' = (a I + P) A (a I + P) = a^2 A + 2 a M + P M, M = P A, and X'' = (a I + P') (a I + P) X =
+    // a^2 X + Q X, Q = a (P + P') + P' P. All of them commute, so each of the five products takes half its tiles:
+    // 3 m^2 n + 5 m^3 multiply-adds where two steps take 6 m^2 n + 2 m^3. As accurate as two steps (the noise of
+    // A's rounding has one step to grow); three steps on one Gram matrix lose a factor of three.
+    constexpr float S_Q = 4096.f;  // |Q| <= a^2 = 11.9
+    MT_TRY(operand_maps(&sq_c, Operand{p.C, p.ld_a, false, p.m}, m));
+    MT_TRY(ns_product(x_short[0], x_short[0], gram_args(m, n, p.A, p.ld_a), st));
+    MT_TRY(ns_product(sq_a, sq_a, poly_args(m, p.A, p.P, p.ld_a, false), st));
+    MT_TRY(ns_product(sq_p, sq_a, square_args(m, p.ld_a, p.C, S_P / (S_P * S_A)), st));  // M
+    NsArgs e = square_args(m, p.ld_a, p.A, S_A / (S_P * S_P));                           // A', over A: a tile adds its own elements
+    e.beta = NS_A * NS_A;
+    e.add_hi = p.A;
+    e.beta_lo = 2.f * NS_A * S_A / S_P;
+    e.add_lo = p.C;
+    MT_TRY(ns_product(sq_p, sq_c, e, st));
+    MT_TRY(ns_product(sq_a, sq_a, poly_args(m, p.A, p.C, p.ld_a, false), st));  // P'
+    e = square_args(m, p.ld_a, p.A, S_Q / (S_P * S_P));                         // Q
+    e.beta = e.beta_lo = NS_A * S_Q / S_P;
+    e.add_hi = p.P;
+    e.add_lo = p.C;
+    MT_TRY(ns_product(sq_c, sq_p, e, st));
+    e = apply_args(m, n, tall, NS_A * NS_A, S_Q, false, c.scale, p.hi[0], p.lo, p.hi[1], two_term > 2 ? p.lo : nullptr, p.ld_x, out,
+                   ld_o, bf_v16);
+    MT_TRY(tall ? ns_product(x_long[0], sq_a, e, st) : ns_product(sq_a, x_long[0], e, st));
+    s = 2;
+  }
+  for (int from = s == 2 ? 1 : 0; s < c.steps; ++s, from ^= 1) {
     const bool fold = s >= two_term, last = s + 1 == c.steps;
-    const CUtensorMap &xs = maps.x_short[s & 1], &xl = maps.x_long[s & 1];
-    MT_TRY(ns_product(xs, tall, xs, tall, gram_args(m, n, p.A, p.ld_a), st));
-    MT_TRY(ns_product(maps.A, false, maps.A, false, poly_args(m, p.A, p.P, p.ld_a, fold), st));
-    const NsArgs e = apply_args(m, n, tall, fold, last, c.scale, p.hi[s & 1], p.lo, p.hi[(s + 1) & 1],
+    MT_TRY(ns_product(x_short[from], x_short[from], gram_args(m, n, p.A, p.ld_a), st));
+    MT_TRY(ns_product(sq_a, sq_a, poly_args(m, p.A, p.P, p.ld_a, fold), st));
+    const NsArgs e = apply_args(m, n, tall, fold ? 0.f : NS_A, S_P, last, c.scale, p.hi[from], p.lo, p.hi[from ^ 1],
                                 s + 1 < two_term ? p.lo : nullptr, p.ld_x, out, ld_o, bf_v16);
-    MT_TRY(tall ? ns_product(xl, false, maps.P, false, e, st) : ns_product(maps.P, false, xl, true, e, st));
+    MT_TRY(tall ? ns_product(x_long[from], sq_p, e, st) : ns_product(sq_p, x_long[from], e, st));
   }
   return MT_OK;
 }

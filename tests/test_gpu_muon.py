@@ -105,9 +105,11 @@ def _check(o, u, cfg):
 
 
 # short sides of the Gram path and around its end, odd sizes, one tile and many, K split over 1 to 8 CTAs,
-# SM pairs (the last ones), each wide and tall
+# SM pairs (the last ones; whole waves of tiles, and a last wave in halves), the first two steps on one Gram matrix
+# (long side at least twice the short one), each wide and tall
 SIZES = [(1, 1), (1, 700), (3, 64), (17, 33), (64, 64), (64, 1111), (63, 5000), (65, 65), (65, 9000), (100, 130), (128, 128), (129, 4100),
-         (200, 210), (256, 688), (300, 1500), (511, 777), (640, 640), (1024, 2560), (1100, 1300), (2300, 2500)]
+         (200, 210), (256, 688), (300, 1500), (511, 777), (640, 640), (1024, 2560), (1100, 1300), (2300, 2500),
+         (2900, 2950), (2850, 5800)]
 
 
 @pytest.mark.parametrize("tall", [False, True])
