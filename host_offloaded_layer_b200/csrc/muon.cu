@@ -569,27 +569,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   wait_for_last();
 
   if (warp == 0) {
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = cluster; t < num_tiles && ok; t += n_clusters) {
-      int mb, nb, n0;
-      const bool halved = locate(t, mb, nb, n0);
-      const int m_own = mb * 256 + static_cast<int>(rank) * 128, n_own = n0 + static_cast<int>(rank) * (halved ? 64 : 128);
-      for (int kb = 0; kb < num_kb; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!warp_wait(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = cluster; t < num_tiles && ok; t += n_clusters) {
+        int mb, nb, n0;
+        const bool halved = locate(t, mb, nb, n0);
+        const int m_own = mb * 256 + static_cast<int>(rank) * 128, n_own = n0 + static_cast<int>(rank) * (halved ? 64 : 128);
+        const uint32_t bytes = rows_bytes(A_MN, mb * 256, ep.M) + rows_bytes(A_MN, mb * 256 + 128, ep.M) +
+                               (halved ? (n0 < ep.N ? MN_BOX : 0) + (n0 + 64 < ep.N ? MN_BOX : 0)
+                                       : rows_bytes(B_MN, n0, ep.N) + rows_bytes(B_MN, n0 + 128, ep.N));
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!wait_one(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
           const uint32_t fb = map_to_rank(smem_u32(&full[s]), 0);
           const int k0 = kb * BK, atoms = min(KA, (ep.K - k0 + 63) / 64);
-          if (rank == 0) {
-            const uint32_t bytes = rows_bytes(A_MN, mb * 256, ep.M) + rows_bytes(A_MN, mb * 256 + 128, ep.M) +
-                                   (halved ? (n0 < ep.N ? MN_BOX : 0) + (n0 + 64 < ep.N ? MN_BOX : 0)
-                                           : rows_bytes(B_MN, n0, ep.N) + rows_bytes(B_MN, n0 + 128, ep.N));
-            mbar_expect_tx(smem_u32(&full[s]), bytes * static_cast<uint32_t>(atoms));
-          }
+          if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), bytes * static_cast<uint32_t>(atoms));
           auto load = [&](const CUtensorMap* map) {
             return [=](uint32_t dst, int c0, int c1) {
               asm volatile(
@@ -612,11 +610,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
             }
           }
         }
-        __syncwarp();
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && lane == 0) {
       constexpr uint16_t both = 0x3;
       auto commit = [&](uint64_t* bar) {
         asm volatile(
@@ -625,41 +623,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
             "h"(both)
             : "memory");
       };
+      const uint64_t a_desc = stage_desc<A_MN, KA>(smem_u32(sA)), b_desc = stage_desc<B_MN, KA>(smem_u32(sB));
       uint32_t it = 0;
       int tl = 0;
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++tl) {
         const int ab = tl & 1;
         const uint32_t idesc = t < ep.full_tiles ? idesc_f16(256, 256, A_MN, B_MN) : idesc_f16(256, 128, A_MN, B_MN);
-        if (!warp_wait(smem_u32(&tempty[ab]), ((tl >> 1) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) break;
+        if (!wait_one(smem_u32(&tempty[ab]), ((tl >> 1) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) break;
         fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(ab * 256);
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const int s = it % STAGES;
-          if (!warp_wait(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
+          if (!wait_one(smem_u32(&full[s]), (it / STAGES) & 1u, abort_flag, err, DEV_ERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
           fence_after();
-          if (lane == 0) {
-            const uint64_t ad = stage_desc<A_MN, KA>(smem_u32(sA + s * OP_STAGE)), bd = stage_desc<B_MN, KA>(smem_u32(sB + s * OP_STAGE));
-            const int ksteps = 4 * min(KA, (ep.K - kb * BK + 63) / 64);
-            for (int kk = 0; kk < ksteps; ++kk)
+          const uint64_t ad = a_desc + s * (OP_STAGE >> 4), bd = b_desc + s * (OP_STAGE >> 4);
+          const int atoms = min(KA, (ep.K - kb * BK + 63) / 64);
+#pragma unroll
+          for (int kk = 0; kk < 4 * KA; ++kk)
+            if (kk < 4 * atoms)
               asm volatile(
                   "{\n\t.reg .pred p;\n\t"
                   "setp.ne.b32 p, %4, 0;\n\t"
                   "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                  "l"(ad + step_off<A_MN>(kk)), "l"(bd + step_off<B_MN>(kk)), "r"(idesc),
-                  "r"((kb > 0 || kk > 0) ? 1u : 0u));
-            commit(&empty[s]);
-          }
-          __syncwarp();
+                  "l"(ad + step_off<A_MN>(kk)), "l"(bd + step_off<B_MN>(kk)), "r"(idesc), "r"((kb > 0 || kk > 0) ? 1u : 0u));
+          commit(&empty[s]);
         }
-        if (!ok) break;
-        if (lane == 0) commit(&tfull[ab]);
-        __syncwarp();
+        if (ok) commit(&tfull[ab]);
       }
     }
+    __syncwarp();
   } else {
     const int q = warp & 3;  // TMEM lanes [32 q, 32 q + 32)
     uint16_t* stage = reinterpret_cast<uint16_t*>(smem + RING + 256 + q * STAGE_BYTES);
