@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "mt_internal.h"
+#include "tcgen05.cuh"
 #include "vec.cuh"
 
 namespace mt {
@@ -61,6 +62,13 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* p, int byte
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// `bytes` (a multiple of 16) from global to shared memory, counted by the barrier at `bar`; all 16-byte aligned.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* p, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(p),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 }
@@ -131,6 +139,13 @@ struct Cols {
   }
   // bf16 values of a vector over the columns (gain or bias), `fill` where there are none
   __device__ __forceinline__ void gather(int k, const __nv_bfloat16* p, float fill, f2 (&v)[4]) const {
+    if (!EDGE && p && any(k) && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      uint32_t w[4];
+      words(__ldg(reinterpret_cast<const uint4*>(p + col[k])), w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_of(w[i]);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int a = 2 * i, b = 2 * i + 1;
@@ -312,9 +327,63 @@ struct LnBwd {
   float *dg, *db;
   int64_t ld_dy, ld_x, ld_dres, ld_dx, rows, stride;
   int64_t hop_dy, hop_x, hop_dres, hop_dx;
-  int H, W;
+  int H, W, slots;
   float inv_h;
+  int32_t* err;
 };
+
+// The column sums of the CTA's groups, added in group order (groups may hold other columns: the sums meet by column),
+// into the CTA's partial row.
+template <int NV, bool EDGE>
+__device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>& cols, float* sums, int group, int groups,
+                                           const f2 (&dg)[NV][4], const f2 (&db)[NV][4]) {
+  float* pg = gridDim.x == 1 ? a.dg : a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+  float* pb = gridDim.x == 1 ? a.db : pg + a.H;
+  for (int gi = 0; gi < groups; ++gi) {
+    if (gi > 0) __syncthreads();
+    if (group == gi) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (!EDGE && groups == 1 && gridDim.x > 1) {  // whole vectors of 16-byte aligned rows
+          if (cols.any(k)) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              float v[4];
+              f2_split(dg[k][i], v[0], v[1]);
+              f2_split(dg[k][i + 1], v[2], v[3]);
+              *reinterpret_cast<float4*>(pg + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+              f2_split(db[k][i], v[0], v[1]);
+              f2_split(db[k][i + 1], v[2], v[3]);
+              *reinterpret_cast<float4*>(pb + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+          }
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= cols.lo[k] && i < cols.hi[k]) {
+            float vg[2], vb[2];
+            f2_split(dg[k][i / 2], vg[0], vg[1]);
+            f2_split(db[k][i / 2], vb[0], vb[1]);
+            float sg = vg[i & 1], sb = vb[i & 1];
+            const int j = cols.col[k] + i;
+            if (gi > 0) {
+              sg += sums[j];
+              sb += sums[a.H + j];
+            }
+            if (gi + 1 < groups) {
+              sums[j] = sg;
+              sums[a.H + j] = sb;
+            } else {
+              if (pg) pg[j] = sg;
+              if (pb) pb[j] = sb;
+            }
+          }
+        }
+      }
+    }
+  }
+}
 
 // A row at a time, the next ones in flight.
 template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
@@ -427,39 +496,145 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // the groups' sums, added in group order (groups of one CTA may hold other columns: the sums meet by column)
-  float* sums = reinterpret_cast<float*>(smem);
-  float* pg = gridDim.x == 1 ? a.dg : a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  float* pb = gridDim.x == 1 ? a.db : pg + a.H;
-  for (int gi = 0; gi < groups; ++gi) {
-    if (gi > 0) __syncthreads();
-    if (group == gi) {
+  leave_sums<NV, EDGE>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db);
+}
+
+// Rows of whole granules: R rows of a group at a time, through a ring of `slots` rows (a multiple of R, 2 R at least:
+// the slots of the R rows before are filled while R are worked on) that bulk copies fill (one an
+// operand and row, issued by the group's first thread, which spares the others the addresses and the instructions).
+// One exchange of sums serves the R rows; what the second half of the work needs is read from the ring again rather
+// than held in registers meanwhile: spilled registers would go to an L1 that the rings leave small.
+constexpr int MAX_SLOTS = 8;
+template <int NV, int R, bool RES, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const __grid_constant__ LnBwd a) {
+
+  constexpr int TENSORS = RES ? 3 : 2;
+  extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [2][H] sums after the rows
+  __shared__ float red[2][32 * 2 * R];
+  __shared__ uint64_t full_bars[8][MAX_SLOTS];
+  __shared__ int abort_word;
+  const int warp = threadIdx.x >> 5, W = a.W, T = W * 32;
+  const int group = warp / W, wig = warp - group * W, groups = blockDim.x / T;
+  const int t = threadIdx.x - group * T;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const Cols<NV, false> cols(t, T, 0, a.H);
+  const uint32_t slice = static_cast<uint32_t>(T) * NV * 16, slot_bytes = TENSORS * slice;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + group * a.slots * slot_bytes + t * 16;
+  const uint32_t full = tc::smem_u32(&full_bars[group][0]);
+  if (t == 0)
+    for (int s = 0; s < a.slots; ++s) tc::mbar_init(full + 8 * s, 1);
+  if (threadIdx.x == 0) abort_word = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // into slot s, by the group's first thread
+  auto fill = [&](int64_t row, int s) {
+    if (t == 0 && row < a.rows) {
+      const uint32_t bytes = static_cast<uint32_t>(a.H) * 2, to = ring + s * slot_bytes, bar = full + 8 * s;
+      tc::mbar_expect_tx(bar, bytes * TENSORS);
+      bulk_copy(to, a.dy + row * a.ld_dy, bytes, bar);
+      bulk_copy(to + slice, a.x + row * a.ld_x, bytes, bar);
+      if (RES) bulk_copy(to + 2 * slice, a.dres + row * a.ld_dres, bytes, bar);
+    }
+  };
+  for (int s = 0; s < a.slots; ++s) fill(first + s * a.stride, s);  // its own barriers: initialised by this thread
+  f2 dg[NV][4], db[NV][4], gain[NV][4];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
+  for (int k = 0; k < NV; ++k) {
+    cols.gather(k, a.g, 1.f, gain[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= cols.lo[k] && i < cols.hi[k]) {
-            float vg[2], vb[2];
-            f2_split(dg[k][i / 2], vg[0], vg[1]);
-            f2_split(db[k][i / 2], vb[0], vb[1]);
-            float sg = vg[i & 1], sb = vb[i & 1];
-            const int j = cols.col[k] + i;
-            if (gi > 0) {
-              sg += sums[j];
-              sb += sums[a.H + j];
-            }
-            if (gi + 1 < groups) {
-              sums[j] = sg;
-              sums[a.H + j] = sb;
-            } else {
-              if (pg) pg[j] = sg;
-              if (pb) pb[j] = sb;
-            }
+    for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0;
+  }
+  cols.clear_absent(ring, T, a.slots * TENSORS, slice);  // behind what a copy writes
+  __syncthreads();
+  float next_mean[R], next_rstd[R];
+  auto stats = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = row + r * a.stride < a.rows;
+      next_mean[r] = live ? a.mean[row + r * a.stride] : 0.f;
+      next_rstd[r] = live ? a.rstd[row + r * a.stride] : 0.f;
+    }
+  };
+  stats(first);
+  int slot = 0, buf = 0;  // a.slots is a multiple of R
+  uint32_t phase = 0;
+  __nv_bfloat16* out = a.dx + first * a.ld_dx;
+  for (int64_t row = first; row < a.rows; row += R * a.stride) {
+    float s[2 * R];
+    f2 rs[R], off[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rs[r] = f2_both(next_rstd[r]);
+      off[r] = f2_both(-next_mean[r] * next_rstd[r]);
+    }
+    stats(row + R * a.stride);
+    const uint32_t at = ring + slot * slot_bytes;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f2 s0 = 0, s1 = 0;
+      if (row + r * a.stride < a.rows) {
+        // bounded; if it runs out, the error word is set and the rows go on without what did not arrive
+        if (!tc::mbar_try(full + 8 * (slot + r), phase))
+          tc::mbar_wait(full + 8 * (slot + r), phase, &abort_word, a.err, DEV_ERR_TIMEOUT_PRODUCER);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          uint32_t d[4], x[4];
+          lds128(at + r * slot_bytes + k * T * 16, d);
+          lds128(at + r * slot_bytes + slice + k * T * 16, x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f2 dv = f2_of(d[i]), xh = f2_fma(f2_of(x[i]), rs[r], off[r]), w = f2_mul(dv, gain[k][i]);
+            s0 = f2_add(s0, w);
+            s1 = f2_fma(w, xh, s1);
+            dg[k][i] = f2_fma(dv, xh, dg[k][i]);
+            db[k][i] = f2_add(db[k][i], dv);
           }
         }
       }
+      s[2 * r] = f2_sum(s0);
+      s[2 * r + 1] = f2_sum(s1);
+    }
+    group_sums<2 * R>(s, W, wig, 1 + group, red[buf] + group * W * 2 * R);
+    buf ^= 1;
+    // the whole group is behind the rows before these: their slots take the rows a ring's length after them
+    if (row != first) {
+      const int before = slot == 0 ? a.slots - R : slot - R;
+#pragma unroll
+      for (int r = 0; r < R; ++r) fill(row + (a.slots - R + r) * a.stride, before + r);
+    }
+    slot += R;
+    if (slot == a.slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row + r * a.stride < a.rows) {
+        // dx = rstd w - rstd c1 - xh (rstd c2) + dres
+        float rstd, same;
+        f2_split(rs[r], rstd, same);
+        const f2 k1 = f2_both(-rstd * (s[2 * r] * a.inv_h)), k2 = f2_both(-rstd * (s[2 * r + 1] * a.inv_h));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          uint32_t o[4], q[4], d[4], x[4];
+          lds128(at + r * slot_bytes + k * T * 16, d);
+          lds128(at + r * slot_bytes + slice + k * T * 16, x);
+          if (RES) lds128(at + r * slot_bytes + 2 * slice + k * T * 16, q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f2 v = f2_fma(f2_fma(f2_of(x[i]), rs[r], off[r]), k2, k1);
+            v = f2_fma(f2_mul(f2_of(d[i]), gain[k][i]), rs[r], v);
+            if (RES) v = f2_add(v, f2_of(q[i]));
+            o[i] = f2_pack(v);
+          }
+          cols.store(k, out, o);
+        }
+      }
+      out += a.hop_dx;
     }
   }
+  __syncthreads();
+  leave_sums<NV, false>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db);
 }
 
 // dg and db from `parts` partial rows of 2H floats: 32 columns a block, 32 threads a column, each the sum of
@@ -567,15 +742,19 @@ Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_
   return s;
 }
 
-constexpr int FWD_THREADS_SM = 512, BWD_THREADS_SM = 512;
+constexpr int FWD_THREADS_SM = 512;
 
-// The backward's registers (128 a thread with two vectors) leave room for two CTAs of up to 256 threads, rows of up
-// to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps on the SM than two vectors
-// and 320 of 128 do (32768 x 5120: 214 us against 228). Fewer registers spill into an L1 that the rings leave
-// small: 330 us.
 Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
-  const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
-  return shape_of(rows, H, g, vecs > 512 && vecs <= 640 ? 640 : 32, BWD_THREADS_SM, 1, res ? 3 : 2);
+  if (g.shifted() || H % 8) {
+    // Rows of partial granules, registers of 128 a thread with two vectors: two CTAs of up to 256 threads, rows of up
+    // to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps on the SM.
+    const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
+    return shape_of(rows, H, g, vecs > 512 && vecs <= 640 ? 640 : 32, 512, 1, res ? 3 : 2);
+  }
+  // whole granules: 128 registers a thread, 512 threads an SM; or, rows of 4097 to 5120, two CTAs of up to 320 threads of
+  // 96 (32768 x 5120: 188 us, against 204 with one CTA of 128)
+  const Shape s = shape_of(rows, H, g, 32, 512, 1, res ? 3 : 2);
+  return s.threads > 256 && s.threads <= 320 ? shape_of(rows, H, g, 32, 640, 1, res ? 3 : 2) : s;
 }
 
 template <int NV, bool EDGE, int THREADS, int CTAS>
@@ -624,20 +803,53 @@ uint64_t bwd_ws_bytes(int64_t rows, int H) {
   return static_cast<uint64_t>(align_up(static_cast<int64_t>(std::max(1, bwd_parts(rows, H))) * 2 * H * 4, 256));
 }
 
-template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
+template <int NV, bool RES, int THREADS, int CTAS>
 mt_status bwd_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
   static SmemOptIn opt;
-  auto* kernel = layernorm_bwd_kernel<NV, EDGE, RES, THREADS, CTAS>;
+  auto* kernel = layernorm_bwd_kernel<NV, true, RES, THREADS, CTAS>;
   const int64_t smem = std::max<int64_t>(s.smem, s.groups > 1 ? 2ll * a.H * 4 : 0);
   if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(kernel)));
   kernel<<<s.ctas, s.threads, smem, st>>>(a);
   return launch_check("layernorm_bwd_kernel");
 }
 
-template <bool EDGE, bool RES>
-mt_status bwd_shape_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
-  if (s.nv == 1) return s.threads <= 320 ? bwd_go<1, EDGE, RES, 320, 2>(a, s, st) : bwd_go<1, EDGE, RES, 640, 1>(a, s, st);
-  return s.threads <= 256 ? bwd_go<2, EDGE, RES, 256, 2>(a, s, st) : bwd_go<2, EDGE, RES, 512, 1>(a, s, st);
+template <bool RES>
+mt_status bwd_edge_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
+  if (s.nv == 1) return s.threads <= 320 ? bwd_go<1, RES, 320, 2>(a, s, st) : bwd_go<1, RES, 640, 1>(a, s, st);
+  return s.threads <= 256 ? bwd_go<2, RES, 256, 2>(a, s, st) : bwd_go<2, RES, 512, 1>(a, s, st);
+}
+
+template <int NV, int R, bool RES, int THREADS, int CTAS>
+mt_status bwd_bulk_rows_go(LnBwd a, const Shape& s, int64_t slot, cudaStream_t st) {
+  static SmemOptIn opt;
+  auto* kernel = layernorm_bwd_bulk_kernel<NV, R, RES, THREADS, CTAS>;
+  const int64_t smem = std::max<int64_t>(slot * a.slots, s.groups > 1 ? 2ll * a.H * 4 : 0);
+  if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(kernel)));
+  kernel<<<s.ctas, s.threads, smem, st>>>(a);
+  return launch_check("layernorm_bwd_bulk_kernel");
+}
+
+// The ring holds as many rows as the SM's shared memory has for its CTAs: two at a time need four (the slots of the
+// two before are filled while two are worked on), one at a time two.
+template <int NV, bool RES, int THREADS, int CTAS>
+mt_status bwd_bulk_go(LnBwd a, const Shape& s, cudaStream_t st) {
+  const int64_t slot = static_cast<int64_t>(s.threads) * NV * 16 * (RES ? 3 : 2);
+  const int resident = std::max(1, std::min(CTAS * THREADS / s.threads, 8));
+  const int fit = static_cast<int>(std::min<int64_t>(MAX_SLOTS, (220 * 1024 / resident - 2048) / slot));
+  if constexpr (NV == 2 && THREADS == 320) {  // two rows' values do not fit its registers: 188 us one at a time, 198 two
+    a.slots = std::max(2, fit);
+    return bwd_bulk_rows_go<NV, 1, RES, THREADS, CTAS>(a, s, slot, st);
+  } else {
+    a.slots = std::max(4, fit & ~1);
+    return bwd_bulk_rows_go<NV, 2, RES, THREADS, CTAS>(a, s, slot, st);
+  }
+}
+
+template <bool RES>
+mt_status bwd_whole_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
+  if (s.nv == 1) return bwd_bulk_go<1, RES, 320, 2>(a, s, st);
+  if (s.threads <= 256) return bwd_bulk_go<2, RES, 256, 2>(a, s, st);
+  return s.threads <= 320 ? bwd_bulk_go<2, RES, 320, 2>(a, s, st) : bwd_bulk_go<2, RES, 512, 1>(a, s, st);
 }
 
 mt_status layernorm_bwd_launch(LnBwd a, cudaStream_t st) {
@@ -669,10 +881,12 @@ mt_status layernorm_bwd_launch(LnBwd a, cudaStream_t st) {
     a.hop_dres = a.stride * a.ld_dres;
     a.hop_dx = a.stride * a.ld_dx;
     parts = s.ctas;
+    a.err = device_error_word();
+    if (!a.err) return fail(MT_ERR_CUDA, "device error word unavailable");
     if (g.shifted() || a.H % 8)
-      MT_TRY((a.dres ? bwd_shape_go<true, true>(a, s, st) : bwd_shape_go<true, false>(a, s, st)));
+      MT_TRY((a.dres ? bwd_edge_go<true>(a, s, st) : bwd_edge_go<false>(a, s, st)));
     else
-      MT_TRY((a.dres ? bwd_shape_go<false, true>(a, s, st) : bwd_shape_go<false, false>(a, s, st)));
+      MT_TRY((a.dres ? bwd_whole_go<true>(a, s, st) : bwd_whole_go<false>(a, s, st)));
     if (parts == 1) return MT_OK;
   }
   if (!a.dg && !a.db) return MT_OK;
@@ -767,6 +981,8 @@ mt_status mt_layernorm_bwd(const mt_bf16* dy, int64_t ld_dy, const mt_bf16* x, i
   a.W = 0;
   a.stride = 0;
   a.inv_h = 1.0f / static_cast<float>(H);
+  a.slots = 0;
+  a.err = nullptr;
   return layernorm_bwd_launch(a, as_stream(stream));
 }
 

@@ -114,30 +114,26 @@ __device__ __forceinline__ void words(const uint4& u, uint32_t (&w)[4]) {
   w[3] = u.w;
 }
 
-// Sums of N values (N = 1, 2 or 4) over the warp, left in every lane. The first log2(N) exchanges halve the
+// Sums of N values (N = 1, 2, 4 or 8) over the warp, left in every lane. The first log2(N) exchanges halve the
 // number of values a lane carries, so N = 4 takes 10 shuffles instead of 20; the order of additions is fixed.
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N]) {
-  static_assert(N == 1 || N == 2 || N == 4, "");
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
   constexpr unsigned ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  float s;
-  if constexpr (N == 4) {
-    const bool hi = lane & 16;
-    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(ALL, hi ? v[0] : v[2], 16);
-    const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(ALL, hi ? v[1] : v[3], 16);
-    const bool h2 = lane & 8;
-    s = (h2 ? b : a) + __shfl_xor_sync(ALL, h2 ? a : b, 8);
-  } else if constexpr (N == 2) {
-    const bool hi = lane & 16;
-    s = (hi ? v[1] : v[0]) + __shfl_xor_sync(ALL, hi ? v[0] : v[1], 16);
-    s += __shfl_xor_sync(ALL, s, 8);
-  } else {
-    s = v[0] + __shfl_xor_sync(ALL, v[0], 16);
-    s += __shfl_xor_sync(ALL, s, 8);
-  }
+  int o = 16;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(ALL, s, o);
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = hi ? v[n + i] : v[i], give = hi ? v[i] : v[n + i];
+      v[i] = keep + __shfl_xor_sync(ALL, give, o);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (int p = 16 / N; p > 0; p /= 2) s += __shfl_xor_sync(ALL, s, p);
   if constexpr (N == 1) {
     v[0] = s;
   } else {

@@ -53,7 +53,7 @@ LN_SIZES = [(1, 1, 1, 0), (5, 2, 2, 0), (3, 7, 9, 1), (1, 8, 8, 0), (17, 64, 64,
 
 
 @pytest.mark.parametrize("affine", [True, False])
-@pytest.mark.parametrize("rows,width,ld,off", LN_SIZES)
+@pytest.mark.parametrize("rows,width,ld,off", LN_SIZES + [(9000, 256, 256, 0), (4000, 3584, 3584, 0), (2500, 5119, 5121, 0)])
 def test_layernorm_forward(rows, width, ld, off, affine):
     import torch
     gen = torch.Generator().manual_seed(rows * 7919 + width)
@@ -101,8 +101,15 @@ def _ln_bwd_ref(dy, x, mean, rstd, g, dres):
     return xh, w, c1, c2, dx, (dy * xh).sum(0), dy.sum(0), n
 
 
+# many rows for every group, so that each ring goes round: its shapes are those of 8 to 40 warps of one or two vectors, with
+# and without a third operand
+LN_ROUNDS = [(4000, 64, 72, 0), (9000, 256, 256, 0), (5000, 1024, 1024, 0), (3300, 2048, 2048, 0), (2600, 3584, 3584, 0),
+             (2600, 4104, 4104, 0), (2500, 5120, 5120, 0), (1900, 6144, 6144, 0), (1800, 8192, 8192, 0), (2500, 5119, 5121, 0),
+             (1800, 8180, 8180, 2), (5001, 777, 777, 0)]
+
+
 @pytest.mark.parametrize("affine,res,alias", [(True, True, None), (True, False, "dy"), (False, True, "dres")])
-@pytest.mark.parametrize("rows,width,ld,off", LN_SIZES + [(0, 24, 24, 0), (4000, 64, 72, 0)])
+@pytest.mark.parametrize("rows,width,ld,off", LN_SIZES + LN_ROUNDS + [(0, 24, 24, 0)])
 def test_layernorm_backward(rows, width, ld, off, affine, res, alias):
     import torch
     gen = torch.Generator().manual_seed(rows * 7919 + width)
@@ -135,6 +142,7 @@ def test_layernorm_backward(rows, width, ld, off, affine, res, alias):
     chain = rows / 32 + 64 + 4 * 148 / 8
     _within(H.host_f64(dg), rdg, chain * U * np.abs(i64[0] * xh).sum(0) + (np.abs(i64[0]) * dxh).sum(0) + 1e-38)
     _within(H.host_f64(db), rdb, chain * U * np.abs(i64[0]).sum(0) + 1e-38)
+    assert L.mt_device_error(clear=True) == 0  # no wait ran out
     if rows:
         assert _outside_untouched(outs, rows, width, ld, off)
     # again, bit for bit, without the column sums
