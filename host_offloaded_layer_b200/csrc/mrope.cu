@@ -24,7 +24,12 @@ using namespace vec;
 constexpr int MAX_PAIRS = 128, MAX_AXES = 8;
 constexpr int THREADS = 256;
 constexpr int TABLE = 2048;  // (cos, sin) pairs of a tile: 16 KiB
-constexpr int HG = 4;        // heads that share a thread's reads of the table
+// Heads that share a thread's reads of the table, and CTAs of an SM: two heads of 16-byte vectors leave registers for
+// four CTAs (98304 tokens, 32 heads of 128: 276 us against 283 with four heads and three CTAs; 80000 tokens, 5 heads
+// of 80: 40 against 54), narrower vectors want four heads' loads in flight (60000 tokens, 20 heads of 72 in rows of odd
+// stride: 118 us against 178).
+constexpr int heads_a_thread(int vec) { return vec == 8 ? 2 : 4; }
+constexpr int ctas_an_sm(int vec) { return vec == 8 ? 4 : 3; }
 
 struct Mrope {
   const __nv_bfloat16* x;
@@ -54,67 +59,115 @@ __device__ __forceinline__ void turn(typename Raw<VEC>::type& lo, typename Raw<V
   pack(hi, h);
 }
 
-// A thread takes one vector of features of HG heads of a token: their loads are in flight together, and the
-// feature's cos and sin are read from the table once for all of them.
+// A thread takes one vector of features of two or four heads of a token at a time: their loads are in flight together, and
+// the features' cos and sin are read from the table once for all of them. The first ones' loads are issued before
+// the tile's angles are formed.
 template <int VEC>
-__global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ Mrope a) {
+struct Item {
   using V = typename Raw<VEC>::type;
+  static constexpr int HG = heads_a_thread(VEC);
+  V lo[HG], hi[HG];
+  uint32_t tok, v;
+  int n;           // heads
+  int64_t x, y;    // elements from the tile's start
+  __device__ __forceinline__ void load(const Mrope& a, uint32_t it, uint32_t per_token, int rot, int64_t row0) {
+    tok = it / per_token;
+    const uint32_t in_token = it - tok * per_token, hg = in_token / rot;
+    v = in_token - hg * rot;
+    const int64_t at = static_cast<int64_t>(hg) * HG * a.d + v * VEC;
+    x = (row0 + tok) * a.ld_x + at;
+    y = (row0 + tok) * a.ld_y + at;
+    n = min(HG, a.heads - static_cast<int>(hg) * HG);
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      if (h < n) {
+        lo[h] = *reinterpret_cast<const V*>(a.x + x + h * a.d);
+        hi[h] = *reinterpret_cast<const V*>(a.x + x + h * a.d + a.pairs);
+      }
+    }
+  }
+};
+
+template <int VEC>
+__global__ void __launch_bounds__(THREADS, ctas_an_sm(VEC)) mrope_kernel(const __grid_constant__ Mrope a) {
+  using V = typename Raw<VEC>::type;
+  constexpr int HG = heads_a_thread(VEC);
   // cos and sin, [token][feature within a vector][vector]: threads of neighbouring vectors read neighbouring words
   __shared__ float cos_tab[TABLE], sin_tab[TABLE];
   const int rot = a.pairs / VEC;                                // rotated vectors of a head half
   const int tail = a.x == a.y ? 0 : (a.d - 2 * a.pairs) / VEC;  // vectors to copy behind them
   const int head_groups = (a.heads + HG - 1) / HG;
   const int64_t tiles = (a.rows + a.tile - 1) / a.tile;
+  // each lane reads another pair's: from the parameters' constant bank they would come one at a time
+  __shared__ double turns_s[MAX_PAIRS];
+  __shared__ int axis_s[MAX_PAIRS];
+  __shared__ int32_t pos_s[TABLE];  // each place is one thread's own
+  for (int i = threadIdx.x; i < a.pairs; i += THREADS) {
+    turns_s[i] = a.turns[i];
+    axis_s[i] = a.axis[i];
+  }
+  const int tok0 = threadIdx.x / a.pairs, pair0 = threadIdx.x - tok0 * a.pairs, hop = THREADS / a.pairs, leap = THREADS - hop * a.pairs;
   for (int64_t tl = blockIdx.x; tl < tiles; tl += gridDim.x) {
     const int64_t row0 = tl * a.tile;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tile), a.rows - row0));
+    const uint32_t per_token = rot * head_groups, items = tokens * per_token;
+    Item<VEC> item;
+    uint32_t it = threadIdx.x;
+    if (it < items) item.load(a, it, per_token, rot, row0);
     __syncthreads();  // the last tile's table is read
-    for (int e = threadIdx.x; e < tokens * a.pairs; e += THREADS) {
-      const int tok = e / a.pairs, i = e - tok * a.pairs;
-      const double p = static_cast<double>(a.pos[a.axis[i] * a.ld_pos + row0 + tok]) * a.turns[i];
+    // the angles' positions are in flight together; pair i of token tok, `leap` pairs and `hop` tokens on for each
+    constexpr int N = TABLE / THREADS;
+    int tok = tok0, i = pair0;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (tok < tokens) pos_s[threadIdx.x + u * THREADS] = a.pos[axis_s[i] * a.ld_pos + row0 + tok];
+      tok += hop;
+      i += leap;
+      if (i >= a.pairs) {
+        i -= a.pairs;
+        ++tok;
+      }
+    }
+    tok = tok0;
+    i = pair0;
+    for (int e = threadIdx.x; tok < tokens; e += THREADS) {  // e = tok * pairs + i
+      const double p = static_cast<double>(pos_s[e]) * turns_s[i];
       float s, c;
       sincospif(2.0f * static_cast<float>(p - rint(p)), &s, &c);
       const int at = tok * a.pairs + (i % VEC) * rot + i / VEC;
       cos_tab[at] = c;
       sin_tab[at] = a.sign * s;
+      tok += hop;
+      i += leap;
+      if (i >= a.pairs) {
+        i -= a.pairs;
+        ++tok;
+      }
     }
     __syncthreads();
-    const uint32_t per_token = rot * head_groups, items = tokens * per_token;
-    for (uint32_t it = threadIdx.x; it < items; it += THREADS) {
-      const uint32_t tok = it / per_token, in_token = it - tok * per_token;
-      const uint32_t hg = in_token / rot, v = in_token - hg * rot;
-      const int64_t at = static_cast<int64_t>(hg) * HG * a.d + v * VEC;
-      const __nv_bfloat16* x = a.x + (row0 + tok) * a.ld_x + at;
-      __nv_bfloat16* y = a.y + (row0 + tok) * a.ld_y + at;
-      const int n = min(HG, a.heads - static_cast<int>(hg) * HG);
-      V lo[HG], hi[HG];
-#pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        if (h < n) {
-          lo[h] = *reinterpret_cast<const V*>(x + h * a.d);
-          hi[h] = *reinterpret_cast<const V*>(x + h * a.d + a.pairs);
-        }
-      }
+    while (it < items) {
       float c[VEC], s[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        c[i] = cos_tab[tok * a.pairs + i * rot + v];
-        s[i] = sin_tab[tok * a.pairs + i * rot + v];
+        c[i] = cos_tab[item.tok * a.pairs + i * rot + item.v];
+        s[i] = sin_tab[item.tok * a.pairs + i * rot + item.v];
       }
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
-        if (h < n) {
-          turn<VEC>(lo[h], hi[h], c, s);
-          *reinterpret_cast<V*>(y + h * a.d) = lo[h];
-          *reinterpret_cast<V*>(y + h * a.d + a.pairs) = hi[h];
+        if (h < item.n) {
+          turn<VEC>(item.lo[h], item.hi[h], c, s);
+          *reinterpret_cast<V*>(a.y + item.y + h * a.d) = item.lo[h];
+          *reinterpret_cast<V*>(a.y + item.y + h * a.d + a.pairs) = item.hi[h];
         }
       }
+      it += THREADS;
+      if (it < items) item.load(a, it, per_token, rot, row0);
     }
     if (tail > 0) {
       const int64_t copies = static_cast<int64_t>(tokens) * a.heads * tail;
-      for (int64_t it = threadIdx.x; it < copies; it += THREADS) {
-        const int64_t th = it / tail, tok = th / a.heads;
-        const int64_t at = (th - tok * a.heads) * a.d + 2 * a.pairs + (it - th * tail) * VEC;
+      for (int64_t k = threadIdx.x; k < copies; k += THREADS) {
+        const int64_t th = k / tail, tok = th / a.heads;
+        const int64_t at = (th - tok * a.heads) * a.d + 2 * a.pairs + (k - th * tail) * VEC;
         *reinterpret_cast<V*>(a.y + (row0 + tok) * a.ld_y + at) =
             *reinterpret_cast<const V*>(a.x + (row0 + tok) * a.ld_x + at);
       }
@@ -124,15 +177,12 @@ __global__ void __launch_bounds__(THREADS) mrope_kernel(const __grid_constant__ 
 
 template <int VEC>
 mt_status go(Mrope a, cudaStream_t st) {
-  const int64_t per_token = static_cast<int64_t>((a.heads + HG - 1) / HG) * (a.pairs / VEC);
-  // tokens of a tile: at least a vector for each thread, no more than the table holds, and no more than leaves
-  // every SM eight tiles
-  const int64_t sms = num_sms();
-  int64_t tile = std::max<int64_t>((THREADS + per_token - 1) / per_token, a.rows / (sms * 8));
-  tile = std::max<int64_t>(1, std::min<int64_t>(tile, TABLE / a.pairs));
-  a.tile = static_cast<int>(tile);
-  const int64_t tiles = (a.rows + tile - 1) / tile;
-  mrope_kernel<VEC><<<static_cast<unsigned>(std::min<int64_t>(tiles, sms * 8)), THREADS, 0, st>>>(a);
+  // as many CTAs as the registers keep resident, tiles of even size: the least number of rounds that the table allows
+  const int64_t ctas = static_cast<int64_t>(num_sms()) * ctas_an_sm(VEC), most = TABLE / a.pairs;
+  const int64_t rounds = (a.rows + ctas * most - 1) / (ctas * most);
+  a.tile = static_cast<int>((a.rows + ctas * rounds - 1) / (ctas * rounds));
+  const int64_t tiles = (a.rows + a.tile - 1) / a.tile;
+  mrope_kernel<VEC><<<static_cast<unsigned>(std::min(tiles, ctas)), THREADS, 0, st>>>(a);
   return launch_check("mrope_kernel");
 }
 
