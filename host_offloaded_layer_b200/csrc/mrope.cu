@@ -28,7 +28,7 @@ constexpr int TABLE = 2048;  // (cos, sin) pairs of a tile: 16 KiB
 // four CTAs (98304 tokens, 32 heads of 128: 276 us against 283 with four heads and three CTAs; 80000 tokens, 5 heads
 // of 80: 40 against 54), narrower vectors want four heads' loads in flight (60000 tokens, 20 heads of 72 in rows of odd
 // stride: 118 us against 178).
-constexpr int heads_a_thread(int vec) { return vec == 8 ? 2 : 4; }
+__host__ __device__ constexpr int heads_a_thread(int vec) { return vec == 8 ? 2 : 4; }
 constexpr int ctas_an_sm(int vec) { return vec == 8 ? 4 : 3; }
 
 struct Mrope {
