@@ -735,8 +735,11 @@ Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_
   const int resident = std::max(1, threads_sm / s.threads);
   const int64_t want = (rows + s.groups - 1) / s.groups;
   int64_t ctas = std::min<int64_t>(want, static_cast<int64_t>(SMS) * resident);
-  // the groups' stride has to be a multiple of the period
-  while (ctas * s.groups % g.period()) ++ctas;
+  // the groups' stride has to be a multiple of the period: fewer CTAs where all are resident, else more
+  if (ctas == static_cast<int64_t>(SMS) * resident)
+    while (ctas * s.groups % g.period()) --ctas;
+  else
+    while (ctas * s.groups % g.period()) ++ctas;
   s.ctas = static_cast<int>(ctas);
   s.smem = static_cast<int64_t>(s.threads) * s.nv * 16 * rows_stage * tensors * DEPTH;
   return s;
@@ -767,7 +770,7 @@ mt_status fwd_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
 
 template <bool EDGE>
 mt_status fwd_shape_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
-  if (s.nv == 1) return fwd_go<1, EDGE, 256, 2>(a, s, st);
+  if (s.nv == 1) return s.threads <= 256 ? fwd_go<1, EDGE, 256, 2>(a, s, st) : fwd_go<1, EDGE, 640, 1>(a, s, st);
   return s.threads <= 256 ? fwd_go<2, EDGE, 256, 2>(a, s, st) : fwd_go<2, EDGE, 512, 1>(a, s, st);
 }
 
@@ -782,7 +785,9 @@ mt_status layernorm_fwd_launch(LnFwd a, cudaStream_t st) {
     layernorm_fwd_wide_kernel<<<static_cast<unsigned>(grid), wide_threads(a.H), 0, st>>>(a);
     return launch_check("layernorm_fwd_wide_kernel");
   }
-  const Shape s = shape_of(a.rows, a.H, g, 32, FWD_THREADS_SM, 2, 1);
+  // two vectors a thread; one for rows of 4097 to 5120, whose groups of nine or ten warps would be alone on an SM
+  const int vecs = (a.H + (g.shifted() ? 7 : 0) + 7) / 8;
+  const Shape s = shape_of(a.rows, a.H, g, vecs > 512 && vecs <= 640 ? 640 : 32, FWD_THREADS_SM, 2, 1);
   a.W = s.W;
   a.stride = static_cast<int64_t>(s.ctas) * s.groups;
   a.hop_x = a.stride * a.ld_x;
@@ -795,7 +800,9 @@ int bwd_parts(int64_t rows, int H) {
   const int wide = static_cast<int>(std::min<int64_t>(2 * SMS, (rows + 63) / 64));
   if (H > MAX_H_REG) return wide;
   int parts = wide;
-  for (int ld = 0; ld < 2; ++ld) parts = std::max(parts, bwd_shape(rows, H, Granules(nullptr, ld), false).ctas);
+  for (uintptr_t base : {uintptr_t(0), uintptr_t(2)})
+    for (int ld : {0, 1, 2, 4})
+      parts = std::max(parts, bwd_shape(rows, H, Granules(reinterpret_cast<const void*>(base), ld), false).ctas);
   return parts;
 }
 

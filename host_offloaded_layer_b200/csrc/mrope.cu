@@ -180,7 +180,9 @@ mt_status go(Mrope a, cudaStream_t st) {
   // as many CTAs as the registers keep resident, tiles of even size: the least number of rounds that the table allows
   const int64_t ctas = static_cast<int64_t>(num_sms()) * ctas_an_sm(VEC), most = TABLE / a.pairs;
   const int64_t rounds = (a.rows + ctas * most - 1) / (ctas * most);
-  a.tile = static_cast<int>((a.rows + ctas * rounds - 1) / (ctas * rounds));
+  const int64_t per_token = static_cast<int64_t>(a.pairs / VEC) * ((a.heads + heads_a_thread(VEC) - 1) / heads_a_thread(VEC));
+  // (a tile's items are counted in 32 bits)
+  a.tile = static_cast<int>(std::min<int64_t>((a.rows + ctas * rounds - 1) / (ctas * rounds), std::max<int64_t>(1, (1 << 30) / per_token)));
   const int64_t tiles = (a.rows + a.tile - 1) / a.tile;
   mrope_kernel<VEC><<<static_cast<unsigned>(std::min(tiles, ctas)), THREADS, 0, st>>>(a);
   return launch_check("mrope_kernel");

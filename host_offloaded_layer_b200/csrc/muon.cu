@@ -39,6 +39,7 @@ using namespace tc;
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr float S_X = 16384.f, S_A = 16384.f, S_P = 8192.f;
+constexpr int64_t MAX_ELEMENTS = 1ll << 36;  // no device holds more; sizes and tile numbers stay in range
 constexpr int TINY = 64;  // the widest short side of the Gram path
 
 // ------------------------------------------------------------------ momentum, norm, head and rest of X
@@ -1755,7 +1756,7 @@ using namespace mt;
 extern "C" {
 
 uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || rows >= (1ll << 31) || cols >= (1ll << 31)) return 0;
+  if (rows <= 0 || cols <= 0 || rows >= (1ll << 31) || cols >= (1ll << 31) || rows > MAX_ELEMENTS / cols) return 0;
   return plan(rows, cols, nullptr).bytes;
 }
 
@@ -1767,6 +1768,7 @@ mt_status mt_muon_update(const float* g, int64_t ld_g, const float* m_in, float*
   if (!m_in != !m_out) return fail(MT_ERR_INVALID_ARG, "muon_update: m_in and m_out go together");
   if (rows < 0 || cols < 0 || rows >= (1ll << 31) || cols >= (1ll << 31))
     return fail(MT_ERR_INVALID_ARG, "muon_update: need 0 <= rows, cols < 2^31");
+  if (cols > 0 && rows > MAX_ELEMENTS / cols) return fail(MT_ERR_UNSUPPORTED, "muon_update: more than 2^36 elements");
   if (ld_g < cols || ld_o < cols || (m_in && ld_m < cols))
     return fail(MT_ERR_INVALID_ARG, "muon_update: row stride smaller than cols");
   if (cfg->steps < 1 || cfg->steps > 100) return fail(MT_ERR_INVALID_ARG, "muon_update: 1 to 100 steps, got %d", cfg->steps);

@@ -7,6 +7,10 @@
     python -m host_offloaded_layer_b200.kernel_bench attn_fwd --B 8 --T 1024 --nq 28 --nkv 4 --d 128
     python -m host_offloaded_layer_b200.kernel_bench attn_bwd --B 8 --T 1024 --nq 28 --nkv 4 --d 128
     python -m host_offloaded_layer_b200.kernel_bench rmsnorm --rows 8192 --H 3584
+    python -m host_offloaded_layer_b200.kernel_bench layernorm --rows 8192 --H 3584
+    python -m host_offloaded_layer_b200.kernel_bench layernorm_bwd --rows 8192 --H 3584
+    python -m host_offloaded_layer_b200.kernel_bench mrope --rows 8192 --nq 28 --nkv 4 --d 128
+    python -m host_offloaded_layer_b200.kernel_bench muon --M 3584 --N 18944
     python -m host_offloaded_layer_b200.kernel_bench swiglu --rows 8192 --F 18944
     python -m host_offloaded_layer_b200.kernel_bench layer --hidden 3584 --nq 28 --nkv 4 --d 128 --F 18944 --B 8 --T 1024
 
@@ -35,8 +39,8 @@ def main():
     from host_offloaded_layer_b200 import _lib as L
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("op", choices=["gemm", "gemm_swiglu", "gemm_swiglu_bwd", "attn_fwd", "attn_bwd", "rmsnorm", "swiglu",
-                                   "layer"])
+    ap.add_argument("op", choices=["gemm", "gemm_swiglu", "gemm_swiglu_bwd", "attn_fwd", "attn_bwd", "rmsnorm", "layernorm",
+                                   "layernorm_bwd", "mrope", "muon", "swiglu", "layer"])
     ap.add_argument("--M", type=int, default=8192)
     ap.add_argument("--N", type=int, default=4608)
     ap.add_argument("--K", type=int, default=3584)
@@ -115,6 +119,44 @@ def main():
         fn = lambda: L.mt_rmsnorm_fwd(x, g, y, rstd, a.rows, a.H, 1e-6, st)  # noqa
         work, unit = 4.0 * a.rows * a.H, "GB/s"
         shape = dict(rows=a.rows, H=a.H)
+    elif a.op in ("layernorm", "layernorm_bwd"):
+        x, g, b = _dev(torch, a.rows * a.H, 1), _dev(torch, a.H, 2), _dev(torch, a.H, 3)
+        y = torch.empty_like(x)
+        mean = torch.empty(a.rows, dtype=torch.float32, device="cuda")
+        rstd = torch.empty_like(mean)
+        fwd = lambda: L.mt_layernorm_fwd(x, a.H, g, b, y, a.H, mean, rstd, a.rows, a.H, 1e-6, st)  # noqa: E731
+        fwd()
+        dy = _dev(torch, a.rows * a.H, 4)
+        dg = torch.empty(a.H, dtype=torch.float32, device="cuda")
+        db = torch.empty_like(dg)
+        nws = L.mt_layernorm_bwd_workspace_bytes(a.rows, a.H)
+        ws = torch.empty(nws, dtype=torch.uint8, device="cuda")
+        bwd = lambda: L.mt_layernorm_bwd(dy, a.H, x, a.H, g, mean, rstd, None, 0, y, a.H, dg, db, a.rows, a.H, ws,  # noqa: E731
+                                         nws, st)
+        fn = fwd if a.op == "layernorm" else bwd
+        work, unit = (4.0 if a.op == "layernorm" else 6.0) * a.rows * a.H, "GB/s"
+        shape = dict(rows=a.rows, H=a.H)
+    elif a.op == "mrope":
+        ld, heads = (a.nq + 2 * a.nkv) * a.d, a.nq + a.nkv
+        x = _dev(torch, a.rows * ld, 1)
+        y = torch.empty_like(x)
+        t = torch.arange(a.rows, dtype=torch.int32, device="cuda")
+        pos = torch.stack([t // 1024, t % 1024 // 32, t % 32])
+        sections = [a.d // 8, a.d // 8, a.d // 4]
+        fn = lambda: L.mt_mrope(x, ld, y, ld, pos, a.rows, sections, a.rows, heads, a.d, 1e6, stream=st)  # noqa: E731
+        work, unit = 4.0 * a.rows * heads * a.d, "GB/s"
+        shape = dict(rows=a.rows, nq=a.nq, nkv=a.nkv, d=a.d)
+    elif a.op == "muon":
+        g = _dev(torch, a.M * a.N, 1).float()
+        mom = torch.zeros_like(g)
+        o = torch.empty(a.M * a.N, dtype=torch.bfloat16, device="cuda")
+        mcfg = L.make_muon_cfg()
+        nws = L.mt_muon_workspace_bytes(a.M, a.N)
+        ws = torch.empty(nws, dtype=torch.uint8, device="cuda")
+        fn = lambda: L.mt_muon_update(g, a.N, mom, mom, a.N, o, a.N, a.M, a.N, mcfg, ws, nws, st)  # noqa: E731
+        short, long = sorted((a.M, a.N))
+        work, unit = 5 * (3.0 * short * short * long + 1.0 * short ** 3), "TFLOP/s"  # symmetric products at half
+        shape = dict(M=a.M, N=a.N)
     elif a.op == "swiglu":
         gu = _dev(torch, a.rows * 2 * a.F, 1)
         m = torch.empty(a.rows * a.F, dtype=torch.bfloat16, device="cuda")

@@ -540,7 +540,7 @@ uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols);
  * g, m_in, m_out, o: aligned to their elements (16-byte aligned rows of 4
  * elements, 8 for o, are faster), none overlapping another but m_in = m_out.
  * ws: device, 256-byte aligned, not shared with a call that may run at the same
- * time. Asynchronous on stream. */
+ * time. More than 2^36 elements: MT_ERR_UNSUPPORTED. Asynchronous on stream. */
 mt_status mt_muon_update(const float* g, int64_t ld_g, const float* m_in, float* m_out, int64_t ld_m, mt_bf16* o,
                          int64_t ld_o, int64_t rows, int64_t cols, const mt_muon_cfg* cfg, void* ws, uint64_t ws_bytes,
                          void* stream);

@@ -238,3 +238,31 @@ def test_muon_is_repeatable_on_another_stream_and_in_a_replayed_graph():
         torch.cuda.synchronize()
         assert torch.equal(outs[2][1], -outs[0][1]) and torch.equal(outs[2][0], -outs[0][0])
         del ws1
+
+
+def test_muon_updates_on_two_streams_at_once():
+    """Two updates in flight together (each with its own workspace), of kernels that want every SM: the results of
+    running alone, and no wait that ran out."""
+    import torch
+    shapes = [(300, 1100), (512, 3584), (60, 900), (1024, 2560)]
+    gen = torch.Generator().manual_seed(17)
+    cfg, sets = L.make_muon_cfg(), []
+    for rows, cols in shapes:
+        g, m = _gradient(gen, rows, cols, cols), _gradient(gen, rows, cols, cols)
+        n = L.mt_muon_workspace_bytes(rows, cols)
+        alone = (torch.empty_like(m), H.empty_bf16(rows, cols))
+        _run(g, cols, m, alone[0], cols, alone[1], cols, rows, cols, cfg)
+        sets.append((rows, cols, g, m, alone, [(torch.empty_like(m), H.empty_bf16(rows, cols), H.workspace(n)) for _ in range(2)]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for i in range(len(sets)):
+            for k in range(2):  # different sizes side by side, too
+                rows, cols, g, m, _, outs = sets[(i + k) % len(sets)]
+                mo, o, ws = outs[k]
+                _run(g, cols, m, mo, cols, o, cols, rows, cols, cfg, stream=streams[k], ws=ws)
+    torch.cuda.synchronize()
+    assert L.mt_device_error(clear=True) == 0
+    for rows, cols, g, m, alone, outs in sets:
+        for mo, o, _ in outs:
+            assert torch.equal(mo, alone[0]) and torch.equal(o, alone[1]), (rows, cols)

@@ -347,3 +347,51 @@ def test_calls_on_another_stream_and_in_a_replayed_graph():
     torch.cuda.synchronize()
     for k in ("y", "r", "dx", "mean", "rstd", "dg", "db"):
         assert torch.equal(a[k], want[k]) and torch.equal(b[k], half[k]), k
+
+
+def test_layernorm_passes_on_two_streams_at_once():
+    """Forward and backward of different sizes in flight together, each backward with its own workspace."""
+    import torch
+    gen = torch.Generator().manual_seed(23)
+    sets = []
+    for rows, width in ((4000, 3584), (3000, 777), (2000, 5120), (6000, 256)):
+        x, dy = _rows(gen, rows, width, width)[0], _rows(gen, rows, width, width)[0]
+        n = L.mt_layernorm_bwd_workspace_bytes(rows, width)
+        outs = [dict(y=torch.empty_like(x), dx=torch.empty_like(x), mean=H.empty_f32(rows), rstd=H.empty_f32(rows),
+                     dg=H.empty_f32(width), db=H.empty_f32(width), ws=H.workspace(n)) for _ in range(3)]
+        sets.append((rows, width, x, dy, n, outs))
+
+    def go(s, o, stream):
+        rows, width, x, dy, n, _ = s
+        L.mt_layernorm_fwd(x, width, None, None, o["y"], width, o["mean"], o["rstd"], rows, width, EPS, stream)
+        L.mt_layernorm_bwd(dy, width, x, width, None, o["mean"], o["rstd"], None, 0, o["dx"], width, o["dg"], o["db"], rows, width,
+                           o["ws"], n, stream)
+
+    for s in sets:
+        go(s, s[5][0], None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for i in range(len(sets)):
+            for k in range(2):
+                s = sets[(i + k) % len(sets)]
+                go(s, s[5][1 + k], streams[k])
+    torch.cuda.synchronize()
+    assert L.mt_device_error(clear=True) == 0
+    for s in sets:
+        for o in s[5][1:]:
+            for k in ("y", "dx", "mean", "rstd", "dg", "db"):
+                assert torch.equal(o[k], s[5][0][k]), (s[:2], k)
+
+
+def test_mrope_of_very_wide_rows():
+    """One pair a head and half a million heads: a tile's work passes what few wide heads have."""
+    import torch
+    rows, heads = 5, 500000
+    gen = torch.Generator().manual_seed(29)
+    x, _ = _rows(gen, rows, heads * 2, heads * 2)
+    y, pos = torch.empty_like(x), torch.arange(rows, dtype=torch.int32, device="cuda")
+    L.mt_mrope(x, heads * 2, y, heads * 2, pos, rows, [1], rows, heads, 2, 1e4)
+    torch.cuda.synchronize()
+    ref, mag = _mrope_ref(H.host_f64(x), pos.cpu().numpy()[None], [1], heads, 2, 1e4, 0, 0, 0)
+    _within(H.host_f64(y), ref, UB * np.abs(ref) + 10 * U * mag + 1e-38)

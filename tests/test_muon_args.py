@@ -11,6 +11,7 @@ P = (BUF.ctypes.data + 255) // 256 * 256  # an aligned address that a refused ca
 @pytest.mark.parametrize("bad,name", [
     (dict(g=None), "MT_ERR_INVALID_ARG"), (dict(o=None), "MT_ERR_INVALID_ARG"), (dict(m_in=None), "MT_ERR_INVALID_ARG"),
     (dict(m_out=None), "MT_ERR_INVALID_ARG"), (dict(ws=None), "MT_ERR_INVALID_ARG"), (dict(rows=-1), "MT_ERR_INVALID_ARG"),
+    (dict(rows=1 << 20, cols=(1 << 16) + 1, ld_g=1 << 17, ld_m=1 << 17, ld_o=1 << 17), "MT_ERR_UNSUPPORTED"),
     (dict(cols=1 << 31, ld_g=1 << 32, ld_m=1 << 32, ld_o=1 << 32), "MT_ERR_INVALID_ARG"), (dict(ld_g=7), "MT_ERR_INVALID_ARG"),
     (dict(ld_m=7), "MT_ERR_INVALID_ARG"), (dict(ld_o=7), "MT_ERR_INVALID_ARG"), (dict(cfg=dict(steps=0)), "MT_ERR_INVALID_ARG"),
     (dict(cfg=dict(steps=101)), "MT_ERR_INVALID_ARG"), (dict(cfg=dict(eps=0.0)), "MT_ERR_INVALID_ARG"),
