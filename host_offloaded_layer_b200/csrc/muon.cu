@@ -471,6 +471,16 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
   return mbar_wait(bar, parity, abort_flag, err, code);
 }
 
+// After a wait ran out: the loads that this thread has issued into a ring of `stages` land before the CTA leaves
+// (each waited for at most a second, whatever the abort flag says).
+__device__ __forceinline__ void drain_ring(uint32_t full, uint32_t issued, uint32_t stages) {
+  for (uint32_t g = issued > stages ? issued - stages : 0; g < issued; ++g) {
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try(full + 8 * (g % stages), (g / stages) & 1u))
+      if (globaltimer() - t0 > 1000000000ull) break;
+  }
+}
+
 // Instruction descriptor of kind::f16 with fp16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -569,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   wait_for_last();
 
+  uint32_t issued = 0;  // K stages that the producer has loaded
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
@@ -588,6 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
           const uint32_t fb = map_to_rank(smem_u32(&full[s]), 0);
           const int k0 = kb * BK, atoms = min(KA, (ep.K - k0 + 63) / 64);
+          ++issued;
           if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), bytes * static_cast<uint32_t>(atoms));
           auto load = [&](const CUtensorMap* map) {
             return [=](uint32_t dst, int c0, int c1) {
@@ -697,6 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 
   fence_before();
   __syncthreads();
+  if (*abort_flag && rank == 0) drain_ring(smem_u32(full), issued, STAGES);  // its barriers count both CTAs' loads
   cluster_sync();  // neither CTA leaves while its peer may still signal it
   fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
@@ -711,6 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 constexpr int RED_LD = 132;  // floats of a row of the shared tile: 16-byte accesses of 8 rows hit 32 banks
 static_assert(128 * RED_LD * 4 <= RING, "the tile overlays the ring");
 constexpr int TILE_THREADS = 64 + 256;
+constexpr int FUSED_SMEM = RING + 256 + 8 * STAGE_BYTES + 1024;
 
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
@@ -767,7 +781,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const bool mirror = ep.sym && mb != nb;
   uint16_t* stage = reinterpret_cast<uint16_t*>(smem + 128 * RED_LD * 4 + max(warp - 2, 0) * STAGE_BYTES);  // the ring is read by then
   Addend add[4];
-  bool done = true;  // this warp's waits all ended
+  bool done = true;     // this warp's waits all ended
+  uint32_t issued = 0;  // K atoms that the producer has loaded
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t bytes = rows_bytes(A_MN, mb * 128, ep.M) + rows_bytes(B_MN, nb * 128, ep.N);
@@ -775,6 +790,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const int it = kb - kb0, s = it % STAGES;
         if (!wait_one(smem_u32(&empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
         const uint32_t fb = smem_u32(&full[s]);
+        ++issued;
         mbar_expect_tx(fb, bytes);
         load_atom<A_MN>(smem_u32(sA + s * HALF), MN_BOX, mb * 128, ep.M, kb * 64,
                         [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, &tmA, fb, c0, c1); });
@@ -838,6 +854,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   }
   fence_before();
   __syncthreads();
+  if (*abort_flag) drain_ring(smem_u32(full), issued, STAGES);
   if (size > 1) {
     cluster_sync();
     if (warp >= 2 && done) {
@@ -884,15 +901,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 // ---------------------------------------------------------------- all steps in one kernel
 // Small matrices spend their time between kernels, not in them: 15 products of a few microseconds. Where each
 // product has no more 128 x 128 tiles than about the GPU has SMs, one cooperative kernel (every CTA resident) runs
-// the scaling and all steps, a grid barrier after each. Tiles as in ns_tile_kernel; the Gram products, whose K is
-// the long side, are split over a cluster of CTAs.
+// the scaling and all steps, a grid barrier after each. Tiles as in ns_tile_kernel; K of the Gram products, the long
+// side, is split over CTAs that would have no tile, and a pass over the partial tiles (from L2) finishes them.
 struct FusedArgs {
   Grad grad;
   Walk walk;
   const double* part;
   int parts, vec4;
   double eps;
-  int m, n, tall, steps, two_term, split;  // split: CTAs of a cluster
+  int m, n, tall, steps, two_term, split;  // split: parts of K of a Gram product
+  float* partial;
   __half *hi[2], *lo, *A, *P;
   int64_t ld_x, ld_a;
   float scale;
@@ -906,14 +924,9 @@ struct FusedMaps {
   CUtensorMap x_short[2], x_long[2], A, P;
 };
 
-constexpr int FUSED_ATOMS = 5;                      // K atoms of the ring: 160 KiB
-constexpr int FUSED_RING = FUSED_ATOMS * 2 * HALF;  // its start holds a CTA's shares while they are sent
-constexpr int SHARES = 128 * 128 * 4;               // the shares that a CTA receives: an fp32 tile in all
-constexpr int FUSED_SMEM = FUSED_RING + SHARES + 256 + 1024;
-
 struct TileSmem {
-  uint8_t *sA, *sB, *recv;
-  uint64_t *full, *empty, *tfull, *rfull;
+  uint8_t *sA, *sB, *stages;
+  uint64_t *full, *empty, *tfull;
   volatile int* abort_flag;
   uint32_t tmem;
 };
@@ -944,34 +957,29 @@ __device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned target,
   return *abort_flag == 0;
 }
 
-// Where 16-byte chunk c of a row lies in a block of shares of `share` columns (16, 32 or 64): rows a thread each,
-// eight of them in eight different bank groups.
-__device__ __forceinline__ uint32_t share_at(int row, int c, int share) {
-  const int f = share == 16 ? (row >> 1) & 3 : row & 7;
-  return static_cast<uint32_t>(row * share * 4 + ((c ^ f) << 4));
-}
+// A partial tile in the workspace: eight chunks of 16 columns, each [128 rows][16].
+constexpr int PARTIAL = 128 * 128;
 
-// One product's tiles: `size` CTAs of the cluster share each tile's K (1: each CTA a tile). The CTAs of a split tile
-// send each other their shares of the columns that the other finishes, in bulk copies between shared memories.
-// it: K atoms that this CTA's ring has carried; tiles, splits: (split) tiles that it has finished.
+// One product's tiles over the grid. K of each is split into `split` parts: 1, and the tile is finished here; more,
+// and each part's fp32 sums go to `partial`, in (tile, part) order, for finish_parts behind a grid barrier.
+// it: K atoms that this CTA's ring has carried; tiles: tiles or parts that it has summed (the parity of tfull);
+// issued: atoms that the calling thread has loaded.
 template <bool A_MN, bool B_MN>
-__device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUtensorMap* tmB, const NsArgs& ep, int size,
-                                              const TileSmem& sm, uint32_t& it, uint32_t& tiles, uint32_t& splits, int32_t* err) {
-  constexpr int STAGES = FUSED_ATOMS;
+__device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUtensorMap* tmB, const NsArgs& ep, int split,
+                                              float* partial, const TileSmem& sm, uint32_t& it, uint32_t& tiles, uint32_t& issued, int32_t* err) {
+  constexpr int STAGES = ATOMS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = size > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int num_m = (ep.M + 127) / 128, num_n = (ep.N + 127) / 128;
   const int num_tiles = ep.sym ? num_m * (num_m + 1) / 2 : num_m * num_n;
   const int atoms = (ep.K + 63) / 64;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * rank / size);
-  const int nk = static_cast<int>(static_cast<int64_t>(atoms) * (rank + 1) / size) - kb0;
   const int in_tile = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
-  const int share = 128 / size, count = share >= 32 ? share / 32 : (half == 0 ? 1 : 0);
-  const int step = static_cast<int>(gridDim.x) / size;
-  for (int t = static_cast<int>(blockIdx.x) / size; t < num_tiles; t += step) {
+  for (int u = static_cast<int>(blockIdx.x); u < num_tiles * split; u += static_cast<int>(gridDim.x)) {
+    const int t = u / split, part = u - t * split;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(atoms) * part / split);
+    const int nk = static_cast<int>(static_cast<int64_t>(atoms) * (part + 1) / split) - kb0;  // split <= atoms: never none
     int mb, nb;
     ns_tile(ep, t, num_m, num_n, mb, nb);
-    const int first_col = nb * 128 + rank * share + half * count * 16, row = mb * 128 + in_tile;
+    const int first_col = nb * 128 + half * 64, row = mb * 128 + in_tile;
     const bool mirror = ep.sym && mb != nb, diag = ep.sym && mb == nb;  // on the diagonal both operands are the same rows
     if (warp == 0) {
       if (lane == 0) {
@@ -980,6 +988,7 @@ __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUte
           const uint32_t g = it + i, s = g % STAGES;
           if (!wait_one(smem_u32(&sm.empty[s]), ((g / STAGES) & 1u) ^ 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_PRODUCER)) break;
           const uint32_t fb = smem_u32(&sm.full[s]);
+          ++issued;
           mbar_expect_tx(fb, bytes);
           load_atom<A_MN>(smem_u32(sm.sA + s * HALF), MN_BOX, mb * 128, ep.M, (kb0 + i) * 64,
                           [&](uint32_t dst, int c0, int c1) { tma_load_2d(dst, tmA, fb, c0, c1); });
@@ -1011,80 +1020,34 @@ __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUte
       }
       __syncwarp();
     } else {
-      uint16_t* stage = reinterpret_cast<uint16_t*>(sm.recv + (warp - 2) * STAGE_BYTES);  // products with a result take no shares
+      uint16_t* stage = reinterpret_cast<uint16_t*>(sm.stages + (warp - 2) * STAGE_BYTES);
       Addend add[4];
+      if (split == 1) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < count) load_addend(ep, row, first_col + 16 * c, add[c]);
-      bool done = warp_wait(smem_u32(sm.tfull), tiles & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE);
-      fence_after();
-      const uint32_t tbase = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
-      if (size == 1) {
-        if (done) {
+        for (int c = 0; c < 4; ++c) load_addend(ep, row, first_col + 16 * c, add[c]);
+      }
+      if (warp_wait(smem_u32(sm.tfull), tiles & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE)) {
+        fence_after();
+        const uint32_t tbase = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * 64);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-            tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
+            if (split == 1) {
               const int col0 = first_col + c * 32 + 16 * h;
               float v[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * h + i]);
               if (col0 < ep.N) finish16(ep, row, col0, v, add[2 * c + h], mirror, stage);
-            }
-          }
-        }
-      } else {
-        // every product that read the ring has completed: the shares may overlay it, a block of 128 x share for each CTA
-        if (done) {
+            } else {
+              float4* p = reinterpret_cast<float4*>(partial + static_cast<int64_t>(u) * PARTIAL +
+                                                    ((half * 4 + 2 * c + h) * 128 + in_tile) * 16);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-            tmem_ld32(tbase + static_cast<uint32_t>(c * 32), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int col = half * 64 + c * 32 + 4 * i, to = col / share;
-              *reinterpret_cast<float4*>(sm.sA + to * (128 * 4) * share + share_at(in_tile, (col - to * share) / 4, share)) =
-                  make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
-                              __uint_as_float(r[4 * i + 3]));
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (warp == 2 && lane < size) {
-          if (lane == 0) mbar_expect_tx(smem_u32(sm.rfull), SHARES);
-          const uint32_t block = 128 * 4 * share, to = static_cast<uint32_t>(lane);
-          asm volatile(
-              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                  map_to_rank(smem_u32(sm.recv) + rank * block, to)),
-              "r"(smem_u32(sm.sA) + to * block), "r"(block), "r"(map_to_rank(smem_u32(sm.rfull), to))
-              : "memory");
-        }
-        __syncwarp();
-        done = warp_wait(smem_u32(sm.rfull), splits & 1u, sm.abort_flag, err, DEV_ERR_TIMEOUT_EPILOGUE) && done;
-        if (done) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col0 = first_col + 16 * c;
-            if (c < count && col0 < ep.N) {
-              float v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = 0.f;
-              const int chunk = (half * count + c) * 4;
-              for (int p = 0; p < size; ++p) {
-                const uint8_t* from = sm.recv + p * (128 * 4) * share;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float4 f = *reinterpret_cast<const float4*>(from + share_at(in_tile, chunk + i, share));
-                  v[4 * i] += f.x;
-                  v[4 * i + 1] += f.y;
-                  v[4 * i + 2] += f.z;
-                  v[4 * i + 3] += f.w;
-                }
-              }
-              finish16(ep, row, col0, v, add[c], mirror, stage);
+              for (int i = 0; i < 4; ++i)
+                p[i] = make_float4(__uint_as_float(r[16 * h + 4 * i]), __uint_as_float(r[16 * h + 4 * i + 1]),
+                                   __uint_as_float(r[16 * h + 4 * i + 2]), __uint_as_float(r[16 * h + 4 * i + 3]));
             }
           }
         }
@@ -1093,12 +1056,47 @@ __device__ __forceinline__ void fused_product(const CUtensorMap* tmA, const CUte
     it += static_cast<uint32_t>(nk);
     ++tiles;
     fence_before();
-    if (size > 1) ++splits;
-    if (size > 1 && t + step < num_tiles)
-      cluster_sync();  // the peers have what they were sent, and have read what they received
-    else
-      __syncthreads();  // the accumulator is read
+    __syncthreads();  // the accumulator is read
     fence_after();
+  }
+}
+
+// The tiles of a split symmetric product (no addend) from their parts, added in order: a warp 32 rows of a chunk.
+__device__ __forceinline__ void finish_parts(const NsArgs& ep, int split, const float* partial, const TileSmem& sm) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 2) return;
+  const int num_m = (ep.M + 127) / 128, num_tiles = num_m * (num_m + 1) / 2;
+  Addend none;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) none.hi[i] = none.lo[i] = 0u;
+  for (int w = static_cast<int>(blockIdx.x) * 8 + warp - 2; w < num_tiles * 32; w += static_cast<int>(gridDim.x) * 8) {
+    const int t = w >> 5, quarter = w & 3, chunk = (w >> 2) & 7;
+    int mb, nb;
+    ns_tile(ep, t, num_m, num_m, mb, nb);
+    const int in_tile = quarter * 32 + lane, col0 = nb * 128 + chunk * 16;
+    if (col0 >= ep.N || mb * 128 + quarter * 32 >= ep.M) continue;
+    const float4* p = reinterpret_cast<const float4*>(partial + static_cast<int64_t>(t) * split * PARTIAL + (chunk * 128 + in_tile) * 16);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    for (int s = 0; s < split; s += 4) {  // four parts' loads in flight
+      float4 f[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[q][i] = s + q < split ? p[static_cast<int64_t>(s + q) * (PARTIAL / 4) + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[4 * i] += f[q][i].x;
+          v[4 * i + 1] += f[q][i].y;
+          v[4 * i + 2] += f[q][i].z;
+          v[4 * i + 3] += f[q][i].w;
+        }
+    }
+    finish16(ep, mb * 128 + in_tile, col0, v, none, mb != nb, reinterpret_cast<uint16_t*>(sm.stages));
   }
 }
 
@@ -1109,22 +1107,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSmem sm;
   sm.sA = smem;
-  sm.sB = smem + FUSED_ATOMS * HALF;
-  sm.recv = smem + FUSED_RING;
-  sm.full = reinterpret_cast<uint64_t*>(smem + FUSED_RING + SHARES);
-  sm.empty = sm.full + FUSED_ATOMS;
-  sm.tfull = sm.empty + FUSED_ATOMS;
-  sm.rfull = sm.tfull + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.rfull + 1);
+  sm.sB = smem + ATOMS * HALF;
+  sm.full = reinterpret_cast<uint64_t*>(smem + RING);
+  sm.empty = sm.full + ATOMS;
+  sm.tfull = sm.empty + ATOMS;
+  sm.stages = smem + RING + 256;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.tfull + 1);
   sm.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < FUSED_ATOMS; ++s) {
+    for (int s = 0; s < ATOMS; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     mbar_init(smem_u32(sm.tfull), 1);
-    mbar_init(smem_u32(sm.rfull), 1);
     *sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1141,31 +1137,36 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     scale_pass<4>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
   else
     scale_pass<1>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
-  uint32_t it = 0, tiles = 0, splits = 0;
+  uint32_t it = 0, tiles = 0, issued = 0;
   unsigned target = gridDim.x;
   bool ok = grid_barrier(a.counter, target, sm.abort_flag, err);
   for (int s = 0; s < a.steps && ok; ++s) {
     const __half* x = a.hi[s & 1];
     const bool fold = s >= a.two_term, last = s + 1 == a.steps;
     NsArgs e = gram_args(a.m, a.n, a.A, a.ld_a);
-    fused_product<TALL, TALL>(&maps.x_short[s & 1], &maps.x_short[s & 1], e, a.split, sm, it, tiles, splits, err);
+    fused_product<TALL, TALL>(&maps.x_short[s & 1], &maps.x_short[s & 1], e, a.split, a.partial, sm, it, tiles, issued, err);
+    if (a.split > 1) {
+      ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
+      if (!ok) break;
+      finish_parts(e, a.split, a.partial, sm);
+    }
     ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
     if (!ok) break;
     e = poly_args(a.m, a.A, a.P, a.ld_a, fold);
-    fused_product<false, false>(&maps.A, &maps.A, e, 1, sm, it, tiles, splits, err);
+    fused_product<false, false>(&maps.A, &maps.A, e, 1, nullptr, sm, it, tiles, issued, err);
     ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
     if (!ok) break;
     e = apply_args(a.m, a.n, TALL, fold ? 0.f : NS_A, S_P, last, a.scale, x, a.lo, a.hi[(s + 1) & 1], s + 1 < a.two_term ? a.lo : nullptr, a.ld_x,
                    a.o, a.ld_o, a.bf_v16);
     if (TALL)
-      fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, sm, it, tiles, splits, err);
+      fused_product<false, false>(&maps.x_long[s & 1], &maps.P, e, 1, nullptr, sm, it, tiles, issued, err);
     else
-      fused_product<false, true>(&maps.P, &maps.x_long[s & 1], e, 1, sm, it, tiles, splits, err);
+      fused_product<false, true>(&maps.P, &maps.x_long[s & 1], e, 1, nullptr, sm, it, tiles, issued, err);
     if (!last) ok = grid_barrier(a.counter, target += gridDim.x, sm.abort_flag, err);
   }
   fence_before();
   __syncthreads();
-  if (cluster_size() > 1) cluster_sync();  // no CTA leaves while a peer may still send to it
+  if (*sm.abort_flag) drain_ring(smem_u32(sm.full), issued, ATOMS);
   fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(sm.tmem) : "memory");
 }
@@ -1232,13 +1233,6 @@ mt_status ns_product(const OperandMaps& a, const OperandMaps& b, const NsArgs& e
   if (!a.mn && !b.mn) return ns_launch<false, false>(a.rows128, b.rows128, b.rows64, e, split, st);
   if (!a.mn) return ns_launch<false, true>(a.rows128, b.rows128, b.rows64, e, split, st);
   return ns_launch<true, true>(a.rows128, b.rows128, b.rows64, e, split, st);
-}
-
-// Whether all steps run as one kernel: each product's tiles fit the GPU about once, so that whole SM pairs on
-// 256 x 256 tiles would not be faster.
-bool pick_fused(int m, int n) {
-  const int64_t tm = (m + 127) / 128, tn = (n + 127) / 128;
-  return tm * tn <= num_sms() && tm * (tm + 1) / 2 <= num_sms();
 }
 
 // ------------------------------------------------------------------ short side of at most 64
@@ -1511,11 +1505,30 @@ struct Plan {
   int parts;
   double* part;
   unsigned* counter;
+  int split;       // of the fused kernel's Gram products
+  float* partial;  // and their parts
   __half *hi[2], *lo, *A, *P, *C;  // C: only where the first two steps share a Gram matrix
   double* gram;
   float* r;
   uint64_t bytes;
 };
+
+// Whether all steps run as one kernel: each product's tiles fit a B200 about once, so that whole SM pairs on
+// 256 x 256 tiles would not be faster. (Counted for 148 SMs whatever the device, like the split: a workspace's size
+// and a result's order of sums depend on the matrix alone.)
+constexpr int SMS = 148;
+bool pick_fused(int64_t m, int64_t n) {
+  const int64_t tm = (m + 127) / 128, tn = (n + 127) / 128;
+  return tm * tn <= SMS && tm * (tm + 1) / 2 <= SMS;
+}
+
+// Parts of K of a Gram product in the fused kernel: CTAs without a tile take some, with at least four K atoms a part
+// (a part costs a grid barrier and a pass over the partial tiles, about 4 us in all; an atom 0.2 us).
+int fused_split(int64_t m, int64_t n) {
+  const int64_t tm = (m + 127) / 128, atoms = (n + 63) / 64;
+  const int64_t split = std::min<int64_t>(std::min<int64_t>(SMS / (tm * (tm + 1) / 2), atoms / 4), 16);
+  return atoms - atoms / std::max<int64_t>(1, split) >= 16 ? static_cast<int>(split) : 1;
+}
 
 // Whether the first two steps of a matrix this wide share a Gram matrix: 3 m^2 n of products saved for 3 m^3 more.
 bool pair_first_steps(int64_t m, int64_t n) { return n >= 2 * m; }
@@ -1539,7 +1552,13 @@ Plan plan(int64_t rows, int64_t cols, void* ws) {
     p.lo = b.take<__half>(rows * p.ld_x);
     p.A = b.take<__half>(p.m * p.ld_a);
     p.P = b.take<__half>(p.m * p.ld_a);
-    p.C = pair_first_steps(p.m, p.n) ? b.take<__half>(p.m * p.ld_a) : nullptr;
+    p.split = 1;
+    if (pick_fused(p.m, p.n)) {
+      p.split = fused_split(p.m, p.n);
+      const int64_t tm = (p.m + 127) / 128;
+      if (p.split > 1) p.partial = b.take<float>(tm * (tm + 1) / 2 * p.split * PARTIAL);
+    }
+    p.C = !pick_fused(p.m, p.n) && pair_first_steps(p.m, p.n) ? b.take<__half>(p.m * p.ld_a) : nullptr;
   }
   p.bytes = b.used;
   return p;
@@ -1580,64 +1599,25 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
                       256, 0, 0, st, a);
 }
 
-// Clusters of `split` CTAs that are resident at once (they lie within a GPC: fewer than SMs suggest); asked once a device.
 template <bool TALL>
-mt_status fused_clusters(cudaLaunchConfig_t cfg, int split, int* out) {
-  static std::atomic<int> cache[64][3];
-  int dev = 0, most = 0;
-  MT_CUDA(cudaGetDevice(&dev));
-  std::atomic<int>* known = dev < 64 ? &cache[dev][split == 2 ? 0 : split == 4 ? 1 : 2] : nullptr;
-  if (known) most = known->load(std::memory_order_relaxed);
-  if (most == 0) {
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / split * split), 1, 1);
-    MT_CUDA(cudaOccupancyMaxActiveClusters(&most, ns_fused_kernel<TALL>, &cfg));
-    if (known && most > 0) known->store(most, std::memory_order_relaxed);
-  }
-  *out = most;
-  return MT_OK;
-}
-
-template <bool TALL>
-mt_status fused_launch(const FusedMaps& maps, FusedArgs a, cudaStream_t st) {
+mt_status fused_launch(const FusedMaps& maps, const FusedArgs& a, cudaStream_t st) {
   int32_t* err = device_error_word();
   if (!err) return fail(MT_ERR_CUDA, "device error word unavailable");
   static SmemOptIn opt;
   MT_TRY(opt.raise(reinterpret_cast<const void*>(ns_fused_kernel<TALL>), FUSED_SMEM));
-  // every CTA resident: one an SM. The Gram products, whose K is the long side, are split over the largest cluster
-  // (up to 8) that leaves each CTA four K atoms and the grid a CTA for each tile of the other products; sending the
-  // shares costs about 2 us, a K atom 0.3 us.
-  const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128, gram = tm * (tm + 1) / 2, atoms = (a.n + 63) / 64;
+  // every CTA resident: one an SM, and no more of them than the largest product, or the scaling, has work for
+  const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128;
+  const int64_t want = std::max<int64_t>(std::max<int64_t>(tm * tn, tm * (tm + 1) / 2 * a.split), a.walk.tiles);
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, num_sms())), 1, 1);
   cfg.blockDim = dim3(TILE_THREADS, 1, 1);
   cfg.dynamicSmemBytes = FUSED_SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  a.split = 1;
-  int grid = num_sms();
-  for (int split = 8; split > 1; split /= 2) {
-    if (atoms < split * 4) continue;
-    int clusters = 0;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
-    MT_TRY(fused_clusters<TALL>(cfg, split, &clusters));
-    if (clusters >= gram && clusters * split >= tm * tn) {
-      a.split = split;
-      grid = clusters * split;
-      break;
-    }
-  }
-  attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
-  // no more of them than the largest product, or the scaling, has work for
-  const int64_t want = std::max<int64_t>(std::max<int64_t>(tm * tn, gram * a.split), std::min<int64_t>(a.walk.tiles, num_sms()));
-  grid = static_cast<int>(std::min<int64_t>(grid, (want + a.split - 1) / a.split * a.split));
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.numAttrs = 1;
   MT_CUDA(cudaLaunchKernelEx(&cfg, ns_fused_kernel<TALL>, maps, a, err));
   return launch_check("ns_fused_kernel");
 }
@@ -1687,7 +1667,8 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
     a.tall = tall;
     a.steps = c.steps;
     a.two_term = two_term;
-    a.split = 1;
+    a.split = p.split;
+    a.partial = p.partial;
     a.hi[0] = p.hi[0];
     a.hi[1] = p.hi[1];
     a.lo = p.lo;

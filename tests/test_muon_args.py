@@ -35,12 +35,13 @@ def test_empty_matrices_are_nothing_to_do():
 
 
 def test_workspace_holds_three_copies_of_x_and_its_square_matrices():
-    """Two square matrices, three where the long side is at least twice the short one."""
-    for rows, cols in ((65, 65), (512, 3584), (18944, 3584), (1000, 70), (40000, 300)):
+    """Two square matrices, three where the long side is at least twice the short one; in small matrices, parts of one
+    product (fp32 tiles of 128 x 128) for 148 SMs at most."""
+    for rows, cols in ((65, 65), (512, 3584), (18944, 3584), (1000, 70), (40000, 300), (688, 256)):
         m = min(rows, cols)
         n = L.mt_muon_workspace_bytes(rows, cols)
         up = lambda v: -(-v // 64) * 64  # noqa: E731
-        need = 2 * (3 * rows * up(cols) + (3 if max(rows, cols) >= 2 * m else 2) * m * up(m)) + 592 * 8
-        assert need <= n <= need + 8 * 256
+        need = 2 * (3 * rows * up(cols) + 2 * m * up(m)) + 592 * 8
+        assert need <= n <= need + 2 * m * up(m) + 148 * 128 * 128 * 4 + 9 * 256
     for rows, cols in ((1, 1), (64, 100000), (100000, 3)):
         assert 0 < L.mt_muon_workspace_bytes(rows, cols) <= 148 * 64 * 64 * 8 + 64 * 64 * 4 + 512
