@@ -1522,11 +1522,11 @@ bool pick_fused(int64_t m, int64_t n) {
   return tm * tn <= SMS && tm * (tm + 1) / 2 <= SMS;
 }
 
-// Parts of K of a Gram product in the fused kernel: CTAs without a tile take some, with at least four K atoms a part
+// Parts of K of a Gram product in the fused kernel: CTAs without a tile take some, with at least six K atoms a part
 // (a part costs a grid barrier and a pass over the partial tiles, about 4 us in all; an atom 0.2 us).
 int fused_split(int64_t m, int64_t n) {
   const int64_t tm = (m + 127) / 128, atoms = (n + 63) / 64;
-  const int64_t split = std::min<int64_t>(std::min<int64_t>(SMS / (tm * (tm + 1) / 2), atoms / 4), 16);
+  const int64_t split = std::min<int64_t>(std::min<int64_t>(SMS / (tm * (tm + 1) / 2), atoms / 6), 16);
   return atoms - atoms / std::max<int64_t>(1, split) >= 16 ? static_cast<int>(split) : 1;
 }
 
