@@ -323,7 +323,7 @@ struct LnBwd {
   const float *mean, *rstd;
   const __nv_bfloat16* dres;
   __nv_bfloat16* dx;
-  float* part;  // [gridDim.x][2][H]: partial dg and db; the final dg and db themselves with one CTA
+  float* part;  // [gridDim.x][2][H]: partial dg and db, unless the grid is one CTA
   float *dg, *db;
   int64_t ld_dy, ld_x, ld_dres, ld_dx, rows, stride;
   int64_t hop_dy, hop_x, hop_dres, hop_dx;
@@ -332,56 +332,61 @@ struct LnBwd {
   int32_t* err;
 };
 
-// The column sums of the CTA's groups, added in group order (groups may hold other columns: the sums meet by column),
-// into the CTA's partial row.
+// The column sums of the CTA's groups into the CTA's partial row, or with one CTA into dg and db. sums: [groups][2H]
+// in shared memory (groups may hold other columns, their sums meet by column), added in group order. One group after
+// the other into a single row took 256 x 256 from 4.8 to 8.6 us.
 template <int NV, bool EDGE>
 __device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>& cols, float* sums, int group, int groups,
                                            const f2 (&dg)[NV][4], const f2 (&db)[NV][4]) {
-  float* pg = gridDim.x == 1 ? a.dg : a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  float* pb = gridDim.x == 1 ? a.db : pg + a.H;
-  for (int gi = 0; gi < groups; ++gi) {
-    if (gi > 0) __syncthreads();
-    if (group == gi) {
+  if (!a.dg && !a.db) return;
+  // one group of whole vectors of 16-byte aligned rows: its registers are the partial row
+  const bool direct = !EDGE && groups == 1 && gridDim.x > 1;
+  float* pg = direct ? a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H : sums + group * 2 * a.H;
+  float* pb = pg + a.H;
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (!EDGE && groups == 1 && gridDim.x > 1) {  // whole vectors of 16-byte aligned rows
-          if (cols.any(k)) {
+  for (int k = 0; k < NV; ++k) {
+    if constexpr (!EDGE) {
+      if (!cols.any(k)) continue;
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              float v[4];
-              f2_split(dg[k][i], v[0], v[1]);
-              f2_split(dg[k][i + 1], v[2], v[3]);
-              *reinterpret_cast<float4*>(pg + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
-              f2_split(db[k][i], v[0], v[1]);
-              f2_split(db[k][i + 1], v[2], v[3]);
-              *reinterpret_cast<float4*>(pb + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
-            }
-          }
-          continue;
-        }
+      for (int i = 0; i < 4; i += 2) {
+        float v[4];
+        f2_split(dg[k][i], v[0], v[1]);
+        f2_split(dg[k][i + 1], v[2], v[3]);
+        *reinterpret_cast<float4*>(pg + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+        f2_split(db[k][i], v[0], v[1]);
+        f2_split(db[k][i + 1], v[2], v[3]);
+        *reinterpret_cast<float4*>(pb + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= cols.lo[k] && i < cols.hi[k]) {
-            float vg[2], vb[2];
-            f2_split(dg[k][i / 2], vg[0], vg[1]);
-            f2_split(db[k][i / 2], vb[0], vb[1]);
-            float sg = vg[i & 1], sb = vb[i & 1];
-            const int j = cols.col[k] + i;
-            if (gi > 0) {
-              sg += sums[j];
-              sb += sums[a.H + j];
-            }
-            if (gi + 1 < groups) {
-              sums[j] = sg;
-              sums[a.H + j] = sb;
-            } else {
-              if (pg) pg[j] = sg;
-              if (pb) pb[j] = sb;
-            }
-          }
+      for (int i = 0; i < 8; ++i) {
+        if (i >= cols.lo[k] && i < cols.hi[k]) {
+          float vg[2], vb[2];
+          f2_split(dg[k][i / 2], vg[0], vg[1]);
+          f2_split(db[k][i / 2], vb[0], vb[1]);
+          pg[cols.col[k] + i] = vg[i & 1];
+          pb[cols.col[k] + i] = vb[i & 1];
         }
       }
     }
+  }
+  if (direct) return;
+  const int n = 2 * a.H;
+  auto leave = [&](int j, float v) {
+    if (j < a.H) {
+      if (a.dg) a.dg[j] = v;
+    } else if (a.db) {
+      a.db[j - a.H] = v;
+    }
+  };
+  __syncthreads();
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    float v = sums[j];
+    for (int gi = 1; gi < groups; ++gi) v += sums[gi * n + j];
+    if (gridDim.x == 1)
+      leave(j, v);
+    else
+      a.part[static_cast<int64_t>(blockIdx.x) * n + j] = v;
   }
 }
 
@@ -389,7 +394,7 @@ __device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>&
 template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __grid_constant__ LnBwd a) {
   constexpr int TENSORS = RES ? 3 : 2;
-  extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [2][H] sums after the rows
+  extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [groups][2][H] sums after the rows
   __shared__ float red[2][32 * 2];
   const int warp = threadIdx.x >> 5, W = a.W, T = W * 32;
   const int group = warp / W, wig = warp - group * W, groups = blockDim.x / T;
@@ -509,7 +514,7 @@ template <int NV, int R, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const __grid_constant__ LnBwd a) {
 
   constexpr int TENSORS = RES ? 3 : 2;
-  extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [2][H] sums after the rows
+  extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [groups][2][H] sums after the rows
   __shared__ float red[2][32 * 2 * R];
   __shared__ uint64_t full_bars[8][MAX_SLOTS];
   __shared__ int abort_word;
@@ -810,14 +815,19 @@ uint64_t bwd_ws_bytes(int64_t rows, int H) {
   return static_cast<uint64_t>(align_up(static_cast<int64_t>(std::max(1, bwd_parts(rows, H))) * 2 * H * 4, 256));
 }
 
-template <int NV, bool RES, int THREADS, int CTAS>
-mt_status bwd_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
-  static SmemOptIn opt;
-  auto* kernel = layernorm_bwd_kernel<NV, true, RES, THREADS, CTAS>;
-  const int64_t smem = std::max<int64_t>(s.smem, s.groups > 1 ? 2ll * a.H * 4 : 0);
+// The sums after the rows fit the rings: 8 H bytes a group, against 8 T NV >= H columns of 2 bytes in two operands and
+// two rows at least.
+template <typename Kernel>
+mt_status bwd_launch(Kernel* kernel, SmemOptIn& opt, const LnBwd& a, const Shape& s, int64_t smem, cudaStream_t st) {
   if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(kernel)));
   kernel<<<s.ctas, s.threads, smem, st>>>(a);
   return launch_check("layernorm_bwd_kernel");
+}
+
+template <int NV, bool RES, int THREADS, int CTAS>
+mt_status bwd_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
+  static SmemOptIn opt;
+  return bwd_launch(layernorm_bwd_kernel<NV, true, RES, THREADS, CTAS>, opt, a, s, s.smem, st);
 }
 
 template <bool RES>
@@ -827,13 +837,9 @@ mt_status bwd_edge_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
 }
 
 template <int NV, int R, bool RES, int THREADS, int CTAS>
-mt_status bwd_bulk_rows_go(LnBwd a, const Shape& s, int64_t slot, cudaStream_t st) {
+mt_status bwd_bulk_rows_go(const LnBwd& a, const Shape& s, int64_t slot, cudaStream_t st) {
   static SmemOptIn opt;
-  auto* kernel = layernorm_bwd_bulk_kernel<NV, R, RES, THREADS, CTAS>;
-  const int64_t smem = std::max<int64_t>(slot * a.slots, s.groups > 1 ? 2ll * a.H * 4 : 0);
-  if (smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(kernel)));
-  kernel<<<s.ctas, s.threads, smem, st>>>(a);
-  return launch_check("layernorm_bwd_bulk_kernel");
+  return bwd_launch(layernorm_bwd_bulk_kernel<NV, R, RES, THREADS, CTAS>, opt, a, s, slot * a.slots, st);
 }
 
 // The ring holds as many rows as the SM's shared memory has for its CTAs: two at a time need four (the slots of the
