@@ -171,10 +171,12 @@ struct LnFwd {
   float eps, inv_h;
 };
 
-// Two rows at a time: one exchange of two sums serves both.
-template <int NV, bool EDGE, int THREADS, int CTAS>
+// R rows at a time: one exchange of R sums serves them. Two, where registers allow; rows of 4097 to 5120 would leave
+// one CTA of 320 threads on an SM then, so they go one at a time in two (32768 x 5120: 124 us, against 142 with one
+// vector a thread and 640 threads). A ring that bulk copies fill, as the backward's, was slower here (98304 x 3584:
+// 249 us against 231).
+template <int NV, int R, bool EDGE, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __grid_constant__ LnFwd a) {
-  constexpr int R = 2;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][32 * R];
   const int warp = threadIdx.x >> 5, W = a.W, T = W * 32;
@@ -750,8 +752,6 @@ Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_
   return s;
 }
 
-constexpr int FWD_THREADS_SM = 512;
-
 Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
   if (g.shifted() || H % 8) {
     // Rows of partial granules, registers of 128 a thread with two vectors: two CTAs of up to 256 threads, rows of up
@@ -765,18 +765,19 @@ Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
   return s.threads > 256 && s.threads <= 320 ? shape_of(rows, H, g, 32, 640, 1, res ? 3 : 2) : s;
 }
 
-template <int NV, bool EDGE, int THREADS, int CTAS>
+template <int NV, int R, bool EDGE, int THREADS, int CTAS>
 mt_status fwd_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
   static SmemOptIn opt;
-  if (s.smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(layernorm_fwd_kernel<NV, EDGE, THREADS, CTAS>)));
-  layernorm_fwd_kernel<NV, EDGE, THREADS, CTAS><<<s.ctas, s.threads, s.smem, st>>>(a);
+  if (s.smem > 40 * 1024) MT_TRY(opt.raise(reinterpret_cast<const void*>(layernorm_fwd_kernel<NV, R, EDGE, THREADS, CTAS>)));
+  layernorm_fwd_kernel<NV, R, EDGE, THREADS, CTAS><<<s.ctas, s.threads, s.smem, st>>>(a);
   return launch_check("layernorm_fwd_kernel");
 }
 
 template <bool EDGE>
 mt_status fwd_shape_go(const LnFwd& a, const Shape& s, cudaStream_t st) {
-  if (s.nv == 1) return s.threads <= 256 ? fwd_go<1, EDGE, 256, 2>(a, s, st) : fwd_go<1, EDGE, 640, 1>(a, s, st);
-  return s.threads <= 256 ? fwd_go<2, EDGE, 256, 2>(a, s, st) : fwd_go<2, EDGE, 512, 1>(a, s, st);
+  if (s.nv == 1) return fwd_go<1, 2, EDGE, 256, 2>(a, s, st);
+  if (s.threads <= 256) return fwd_go<2, 2, EDGE, 256, 2>(a, s, st);
+  return s.threads <= 320 ? fwd_go<2, 1, EDGE, 320, 2>(a, s, st) : fwd_go<2, 2, EDGE, 512, 1>(a, s, st);
 }
 
 // Threads of a CTA that walks a row an element at a time.
@@ -790,9 +791,9 @@ mt_status layernorm_fwd_launch(LnFwd a, cudaStream_t st) {
     layernorm_fwd_wide_kernel<<<static_cast<unsigned>(grid), wide_threads(a.H), 0, st>>>(a);
     return launch_check("layernorm_fwd_wide_kernel");
   }
-  // two vectors a thread; one for rows of 4097 to 5120, whose groups of nine or ten warps would be alone on an SM
-  const int vecs = (a.H + (g.shifted() ? 7 : 0) + 7) / 8;
-  const Shape s = shape_of(a.rows, a.H, g, vecs > 512 && vecs <= 640 ? 640 : 32, FWD_THREADS_SM, 2, 1);
+  // 128 registers a thread and 512 threads an SM; rows of 4097 to 5120 in two CTAs of up to 320 threads, of 96 registers
+  Shape s = shape_of(a.rows, a.H, g, 32, 512, 2, 1);
+  if (s.threads > 256 && s.threads <= 320) s = shape_of(a.rows, a.H, g, 32, 640, 1, 1);
   a.W = s.W;
   a.stride = static_cast<int64_t>(s.ctas) * s.groups;
   a.hop_x = a.stride * a.ld_x;
