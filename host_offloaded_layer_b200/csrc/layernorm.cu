@@ -16,10 +16,11 @@
 // The arithmetic is packed (two fp32 a register pair): unpacked, the forward was bound by instruction issue
 // (72% of the slots at 2.2 TB/s of reads).
 //
-// Rows of any alignment take this path. A group's vectors are the 16-byte granules of memory that its rows
-// cover; where H or the row stride is odd, rows start at different places in their first granule, and that
+// Rows of any alignment take this path. A group's vectors are the 16-byte granules of memory that lie whole in
+// its rows; where H or the row stride is odd, rows start at different places in their first granule, and that
 // place (`shift`, in elements) repeats every 8 rows: groups step by multiples of 8 rows, so that each sees one
-// shift and its threads keep their columns. The first and last vector of a row may be partial. (Only operands
+// shift and its threads keep their columns. The up to 14 elements of a row in front of its first and behind its
+// last whole granule go to lanes of the group's last warp, one each, in plain loads and stores. (Only operands
 // whose rows lie differently in their granules go an element at a time.)
 #include <algorithm>
 
@@ -34,7 +35,7 @@ using namespace vec;
 
 constexpr int SMS = 148;            // the partial rows of dg and db are counted for a whole B200, so that sums do not depend on the device
 constexpr int DEPTH = 3;            // stages of a ring: two in flight, one being read
-constexpr int MAX_H_REG = 8192;     // the widest row that 16 warps of two vectors a thread hold (with its shift)
+constexpr int MAX_H_REG = 8192;     // the widest row that 16 warps of two vectors a thread hold
 
 __device__ __forceinline__ void group_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -57,9 +58,9 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int W, int warp_in_gro
   warp_sums<N>(v);
 }
 
-// 16 bytes, or the first `bytes` of them and zeros, from global to shared memory.
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* p, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
+// 16 bytes from global to shared memory.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // `bytes` (a multiple of 16) from global to shared memory, counted by the barrier at `bar`; all 16-byte aligned.
@@ -80,54 +81,31 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 }
 
 // A thread's NV vectors of a row whose first element is the shift-th of its granule: vector t + k T holds the
-// columns col[k] .. col[k] + 7, of which lo[k] .. hi[k] - 1 exist. EDGE = false: rows of whole granules (every
-// vector is full or absent), which spares the checks.
+// columns col[k] .. col[k] + 7, all in the row, or is absent. EDGE: rows may have elements outside their whole
+// granules; edge is the column of one that this lane has, or -1. (A mask for partial vectors instead, in the threads
+// that hold them, made their warp the one that its group waits for: 100000 x 1153 took 159 us, against 97.)
 template <int NV, bool EDGE>
 struct Cols {
-  int col[NV], lo[NV], hi[NV];
+  int col[NV], edge;
+  bool there[NV];
   __device__ __forceinline__ Cols(int t, int T, int shift, int H) {
+    const int head = EDGE ? min((8 - shift) & 7, H) : 0, tail = EDGE ? (H - head) & 7 : 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      col[k] = 8 * (t + k * T) - shift;
-      lo[k] = max(0, -col[k]);
-      hi[k] = min(8, H - col[k]);
-      if (hi[k] <= lo[k]) lo[k] = hi[k] = 0;
+      col[k] = head + 8 * (t + k * T);
+      there[k] = col[k] + 8 <= H;
     }
+    const int e = t - (T - 32);
+    edge = !EDGE || e < 0 || e >= head + tail ? -1 : e < head ? e : H - tail + (e - head);
   }
-  __device__ __forceinline__ bool any(int k) const { return hi[k] > 0; }
-  __device__ __forceinline__ bool partial(int k) const { return EDGE ? hi[k] - lo[k] != 8 : false; }
-  // the vector with zeros outside the row (absent vectors read zeros from the ring already)
-  __device__ __forceinline__ void mask(int k, uint32_t (&w)[4]) const {
-    if (partial(k)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (2 * i < lo[k] || 2 * i >= hi[k]) w[i] &= 0xffff0000u;
-        if (2 * i + 1 < lo[k] || 2 * i + 1 >= hi[k]) w[i] &= 0x0000ffffu;
-      }
-    }
-  }
-  // Starts the copy of a vector of the row `row`, `at` elements into its operand. What lies in front of the row in
-  // its first granule comes along (it belongs to the row before); in front of the operand itself nothing is read.
-  __device__ __forceinline__ void fetch(int k, uint32_t dst, const __nv_bfloat16* row, int64_t at) const {
-    if (!any(k)) return;  // its place in the ring holds zeros from the start
-    if (!EDGE || at + col[k] >= 0) {
-      copy_async(dst, row + col[k], EDGE ? hi[k] * 2 : 16);
-    } else {
-      for (int i = lo[k]; i < hi[k]; ++i)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * i), "h"(reinterpret_cast<const uint16_t*>(row)[col[k] + i])
-                     : "memory");
-    }
+  __device__ __forceinline__ bool any(int k) const { return there[k]; }
+  __device__ __forceinline__ bool has_edge() const { return EDGE && edge >= 0; }
+  // Starts the copy of a vector of the row.
+  __device__ __forceinline__ void fetch(int k, uint32_t dst, const __nv_bfloat16* row) const {
+    if (any(k)) copy_async(dst, row + col[k]);  // an absent one's place in the ring holds zeros from the start
   }
   __device__ __forceinline__ void store(int k, __nv_bfloat16* row, const uint32_t (&w)[4]) const {
-    if (!any(k)) return;
-    if (!partial(k)) {
-      *reinterpret_cast<uint4*>(row + col[k]) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i >= lo[k] && i < hi[k])
-          reinterpret_cast<uint16_t*>(row)[col[k] + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-    }
+    if (any(k)) *reinterpret_cast<uint4*>(row + col[k]) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   // Zeros for the absent vectors of `slots` places of the ring, `pitch` bytes apart.
   __device__ __forceinline__ void clear_absent(uint32_t ring, int T, int slots, uint32_t pitch) const {
@@ -139,7 +117,8 @@ struct Cols {
   }
   // bf16 values of a vector over the columns (gain or bias), `fill` where there are none
   __device__ __forceinline__ void gather(int k, const __nv_bfloat16* p, float fill, f2 (&v)[4]) const {
-    if (!EDGE && p && any(k) && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const bool have = p && any(k);
+    if (!EDGE && have && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
       uint32_t w[4];
       words(__ldg(reinterpret_cast<const uint4*>(p + col[k])), w);
 #pragma unroll
@@ -147,13 +126,18 @@ struct Cols {
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int a = 2 * i, b = 2 * i + 1;
-      v[i] = f2_make(p && a >= lo[k] && a < hi[k] ? __bfloat162float(p[col[k] + a]) : fill,
-                     p && b >= lo[k] && b < hi[k] ? __bfloat162float(p[col[k] + b]) : fill);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = f2_make(have ? __bfloat162float(p[col[k] + 2 * i]) : fill, have ? __bfloat162float(p[col[k] + 2 * i + 1]) : fill);
+  }
+  __device__ __forceinline__ float gather_edge(const __nv_bfloat16* p, float fill) const {
+    return p && has_edge() ? __bfloat162float(p[edge]) : fill;
   }
 };
+
+// A bf16 element's bits, and their value: apart, so that a load in flight is not waited for where it is issued (the
+// forward of 100000 x 1153: 97 us, against 126).
+__device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+__device__ __forceinline__ float as_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
 // The group's place: rows first, first + stride, ... of one shift.
 __device__ __forceinline__ int row_shift(const void* base, int64_t ld, int64_t row) {
@@ -195,21 +179,31 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
     cols.gather(k, a.b, 0.f, bias[k]);
   }
   cols.clear_absent(ring, T, DEPTH * R, slice);
-  int64_t next = first, x_at = first * a.ld_x;  // the row to fetch next and its place
-  const __nv_bfloat16* x_row = a.x + x_at;
+  const float edge_gain = cols.gather_edge(a.g, 1.f), edge_bias = cols.gather_edge(a.b, 0.f);
+  int64_t next = first;  // the row to fetch next
+  const __nv_bfloat16* x_row = a.x + first * a.ld_x;
   auto fill = [&](uint32_t to) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (next < a.rows) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) cols.fetch(k, to + r * slice + k * T * 16, x_row, x_at);
+        for (int k = 0; k < NV; ++k) cols.fetch(k, to + r * slice + k * T * 16, x_row);
       }
       next += a.stride;
       x_row += a.hop_x;
-      x_at += a.hop_x;
     }
     copy_commit();
   };
+  const __nv_bfloat16* edge_at = a.x + first * a.ld_x + cols.edge;  // edge elements are read one turn ahead
+  uint32_t next_edge[R];
+  auto fetch_edge = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      next_edge[r] = cols.has_edge() && row + r * a.stride < a.rows ? bits(edge_at) : 0;
+      if (EDGE) edge_at += a.hop_x;
+    }
+  };
+  fetch_edge(first);
   __nv_bfloat16* out = a.y + first * a.ld_y;
   uint32_t to = ring, at = ring;
   for (int s = 0; s < DEPTH - 1; ++s, to += R * slice) fill(to);
@@ -219,7 +213,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
     if (to == ring_end) to = ring;
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     f2 x[R][NV][4];
-    float s[R];
+    float s[R], edge[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) edge[r] = as_f32(next_edge[r]);
+    fetch_edge(row0 + R * a.stride);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       f2 sum = 0;
@@ -227,7 +224,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
       for (int k = 0; k < NV; ++k) {
         uint32_t w[4];
         lds128(at + r * slice + k * T * 16, w);
-        cols.mask(k, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[r][k][i] = f2_of(w[i]);
@@ -235,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
         }
       }
       s[r] = f2_sum(sum);
+      if (EDGE) s[r] += edge[r];
     }
     at += R * slice;
     if (at == ring_end) at = ring;
@@ -243,26 +240,21 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = s[r] * a.inv_h;
-      const f2 neg = f2_both(-mean[r]);
       f2 sum = 0;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
+        const f2 neg = f2_both(cols.any(k) ? -mean[r] : 0.f);  // absent vectors stay zero
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[r][k][i] = f2_add(x[r][k][i], neg);
-        if (!EDGE && !cols.any(k)) continue;
-        if (cols.partial(k)) {  // what is outside the row adds nothing
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            f2_split(x[r][k][i], lo, hi);
-            x[r][k][i] = f2_make(2 * i >= cols.lo[k] && 2 * i < cols.hi[k] ? lo : 0.f,
-                                 2 * i + 1 >= cols.lo[k] && 2 * i + 1 < cols.hi[k] ? hi : 0.f);
-          }
+        for (int i = 0; i < 4; ++i) {
+          x[r][k][i] = f2_add(x[r][k][i], neg);
+          sum = f2_fma(x[r][k][i], x[r][k][i], sum);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum = f2_fma(x[r][k][i], x[r][k][i], sum);
       }
       q[r] = f2_sum(sum);
+      if (EDGE) {  // no branch: zeros in the other lanes
+        edge[r] -= cols.has_edge() ? mean[r] : 0.f;
+        q[r] = fmaf(edge[r], edge[r], q[r]);
+      }
     }
     group_sums<R>(q, W, wig, 1 + group, red[1] + group * W * R);
 #pragma unroll
@@ -282,6 +274,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
         for (int i = 0; i < 4; ++i) w[i] = f2_pack(f2_fma(f2_mul(x[r][k][i], rs), gain[k][i], bias[k][i]));
         cols.store(k, out, w);
       }
+      if (cols.has_edge()) out[cols.edge] = __float2bfloat16_rn(fmaf(edge[r] * rstd, edge_gain, edge_bias));
       out += a.hop_y;
     }
   }
@@ -339,7 +332,7 @@ struct LnBwd {
 // the other into a single row took 256 x 256 from 4.8 to 8.6 us.
 template <int NV, bool EDGE>
 __device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>& cols, float* sums, int group, int groups,
-                                           const f2 (&dg)[NV][4], const f2 (&db)[NV][4]) {
+                                           const f2 (&dg)[NV][4], const f2 (&db)[NV][4], float edge_dg, float edge_db) {
   if (!a.dg && !a.db) return;
   // one group of whole vectors of 16-byte aligned rows: its registers are the partial row
   const bool direct = !EDGE && groups == 1 && gridDim.x > 1;
@@ -347,30 +340,30 @@ __device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>&
   float* pb = pg + a.H;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if constexpr (!EDGE) {
-      if (!cols.any(k)) continue;
+    if (!cols.any(k)) continue;
+    float vg[8], vb[8];
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        float v[4];
-        f2_split(dg[k][i], v[0], v[1]);
-        f2_split(dg[k][i + 1], v[2], v[3]);
-        *reinterpret_cast<float4*>(pg + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
-        f2_split(db[k][i], v[0], v[1]);
-        f2_split(db[k][i + 1], v[2], v[3]);
-        *reinterpret_cast<float4*>(pb + cols.col[k] + 2 * i) = make_float4(v[0], v[1], v[2], v[3]);
+    for (int i = 0; i < 4; ++i) {
+      f2_split(dg[k][i], vg[2 * i], vg[2 * i + 1]);
+      f2_split(db[k][i], vb[2 * i], vb[2 * i + 1]);
+    }
+    if (!EDGE) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<float4*>(pg + cols.col[k] + i) = make_float4(vg[i], vg[i + 1], vg[i + 2], vg[i + 3]);
+        *reinterpret_cast<float4*>(pb + cols.col[k] + i) = make_float4(vb[i], vb[i + 1], vb[i + 2], vb[i + 3]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i >= cols.lo[k] && i < cols.hi[k]) {
-          float vg[2], vb[2];
-          f2_split(dg[k][i / 2], vg[0], vg[1]);
-          f2_split(db[k][i / 2], vb[0], vb[1]);
-          pg[cols.col[k] + i] = vg[i & 1];
-          pb[cols.col[k] + i] = vb[i & 1];
-        }
+        pg[cols.col[k] + i] = vg[i];
+        pb[cols.col[k] + i] = vb[i];
       }
     }
+  }
+  if (cols.has_edge()) {
+    pg[cols.edge] = edge_dg;
+    pb[cols.edge] = edge_db;
   }
   if (direct) return;
   const int n = 2 * a.H;
@@ -416,30 +409,39 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
     for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0;
   }
   cols.clear_absent(ring, T, DEPTH * TENSORS, slice);
-  // the row to fetch next and its place in each operand
-  int64_t next = first, dy_at = first * a.ld_dy, x_at = first * a.ld_x, res_at = first * a.ld_dres;
-  const __nv_bfloat16 *dy_row = a.dy + dy_at, *x_row = a.x + x_at, *res_row = a.dres + res_at;
+  int64_t next = first;  // the row to fetch next
+  const __nv_bfloat16 *dy_row = a.dy + first * a.ld_dy, *x_row = a.x + first * a.ld_x, *res_row = a.dres + first * a.ld_dres;
   auto fill = [&](uint32_t to) {
     if (next < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const uint32_t dst = to + k * T * 16;
-        cols.fetch(k, dst, dy_row, dy_at);
-        cols.fetch(k, dst + slice, x_row, x_at);
-        if (RES) cols.fetch(k, dst + 2 * slice, res_row, res_at);
+        cols.fetch(k, dst, dy_row);
+        cols.fetch(k, dst + slice, x_row);
+        if (RES) cols.fetch(k, dst + 2 * slice, res_row);
       }
     }
     next += a.stride;
     dy_row += a.hop_dy;
     x_row += a.hop_x;
     if (RES) res_row += a.hop_dres;
-    if (EDGE) {
-      dy_at += a.hop_dy;
-      x_at += a.hop_x;
-      if (RES) res_at += a.hop_dres;
-    }
     copy_commit();
   };
+  // edge elements are read one turn ahead
+  const float edge_gain = cols.gather_edge(a.g, 1.f);
+  float edge_dg = 0.f, edge_db = 0.f;
+  uint32_t next_dy = 0, next_x = 0, next_res = 0;
+  const __nv_bfloat16 *edge_dy_at = dy_row + cols.edge, *edge_x_at = x_row + cols.edge, *edge_res_at = res_row + cols.edge;
+  auto fetch_edge = [&](int64_t row) {
+    const bool live = cols.has_edge() && row < a.rows;
+    next_dy = live ? bits(edge_dy_at) : 0;
+    next_x = live ? bits(edge_x_at) : 0;
+    if (RES) next_res = live ? bits(edge_res_at) : 0;
+    edge_dy_at += a.hop_dy;
+    edge_x_at += a.hop_x;
+    if (RES) edge_res_at += a.hop_dres;
+  };
+  fetch_edge(first);
   __nv_bfloat16* out = a.dx + first * a.ld_dx;
   uint32_t to = ring;
   for (int s = 0; s < DEPTH - 1; ++s, to += TENSORS * slice) fill(to);
@@ -456,46 +458,57 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
       next_mean = a.mean[row + a.stride];
       next_rstd = a.rstd[row + a.stride];
     }
+    const float edge_dy = as_f32(next_dy), edge_x = as_f32(next_x), edge_res = as_f32(next_res);
+    fetch_edge(row + a.stride);
     fill(to);
     to += TENSORS * slice;
     if (to == ring_end) to = ring;
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    f2 xh[NV][4], w[NV][4], s0 = 0, s1 = 0;
+    f2 s0 = 0, s1 = 0;
     const f2 rs = f2_both(rstd), off = f2_both(-mean * rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       uint32_t d[4], x[4];
       lds128(at + k * T * 16, d);
       lds128(at + slice + k * T * 16, x);
-      cols.mask(k, d);  // columns outside the row hold dy = 0 and x = 0: they add nothing to any sum
-      cols.mask(k, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f2 dv = f2_of(d[i]);
-        xh[k][i] = f2_fma(f2_of(x[i]), rs, off);
-        w[k][i] = f2_mul(dv, gain[k][i]);
-        s0 = f2_add(s0, w[k][i]);
-        s1 = f2_fma(w[k][i], xh[k][i], s1);
-        dg[k][i] = f2_fma(dv, xh[k][i], dg[k][i]);
+        const f2 dv = f2_of(d[i]), xh = f2_fma(f2_of(x[i]), rs, off), w = f2_mul(dv, gain[k][i]);
+        s0 = f2_add(s0, w);
+        s1 = f2_fma(w, xh, s1);
+        dg[k][i] = f2_fma(dv, xh, dg[k][i]);
         db[k][i] = f2_add(db[k][i], dv);
       }
     }
+    // absent vectors and the edge elements of other lanes hold dy = 0, which adds nothing to any sum
     float s[2] = {f2_sum(s0), f2_sum(s1)};
+    const float edge_w = edge_dy * edge_gain, edge_xh = fmaf(edge_x, rstd, -mean * rstd);
+    s[0] += edge_w;
+    s[1] = fmaf(edge_w, edge_xh, s[1]);
+    edge_dg = fmaf(edge_dy, edge_xh, edge_dg);
+    edge_db += edge_dy;
     group_sums<2>(s, W, wig, 1 + group, red[buf] + group * W * 2);
     buf ^= 1;
-    // dx = rstd w - rstd c1 - xh (rstd c2) + dres
+    // dx = rstd w - rstd c1 - xh (rstd c2) + dres, from the ring again: registers that held w and xh meanwhile would spill
     const f2 k1 = f2_both(-rstd * (s[0] * a.inv_h)), k2 = f2_both(-rstd * (s[1] * a.inv_h));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      uint32_t o[4], r[4];
+      uint32_t o[4], r[4], d[4], x[4];
+      lds128(at + k * T * 16, d);
+      lds128(at + slice + k * T * 16, x);
       if (RES) lds128(at + 2 * slice + k * T * 16, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f2 v = f2_fma(w[k][i], rs, f2_fma(xh[k][i], k2, k1));
+        f2 v = f2_fma(f2_fma(f2_of(x[i]), rs, off), k2, k1);
+        v = f2_fma(f2_mul(f2_of(d[i]), gain[k][i]), rs, v);
         if (RES) v = f2_add(v, f2_of(r[i]));
         o[i] = f2_pack(v);
       }
       cols.store(k, out, o);
+    }
+    if (cols.has_edge()) {
+      const float v = fmaf(edge_w, rstd, -rstd * (s[0] * a.inv_h) - edge_xh * (rstd * (s[1] * a.inv_h)));
+      out[cols.edge] = __float2bfloat16_rn(RES ? v + edge_res : v);
     }
     out += a.hop_dx;
     at += TENSORS * slice;
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  leave_sums<NV, EDGE>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db);
+  leave_sums<NV, EDGE>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db, edge_dg, edge_db);
 }
 
 // Rows of whole granules: R rows of a group at a time, through a ring of `slots` rows (a multiple of R, 2 R at least:
@@ -641,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
     }
   }
   __syncthreads();
-  leave_sums<NV, false>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db);
+  leave_sums<NV, false>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db, 0.f, 0.f);
 }
 
 // dg and db from `parts` partial rows of 2H floats: 32 columns a block, 32 threads a column, each the sum of
@@ -734,12 +747,19 @@ struct Shape {
 // Works on a whole B200's 148 SMs whatever the device, so that results do not depend on it.
 Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_sm, int rows_stage, int tensors) {
   Shape s;
-  const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
+  const int vecs = std::max(1, H / 8);  // whole granules of a row at most
   s.nv = vecs <= one_vec ? 1 : 2;
   s.W = (vecs + 32 * s.nv - 1) / (32 * s.nv);
   s.groups = std::max(1, 8 / s.W);
   s.threads = s.groups * s.W * 32;
-  const int resident = std::max(1, threads_sm / s.threads);
+  int resident = std::max(1, threads_sm / s.threads);
+  // more groups in one CTA of all the threads (three warps: five groups, against two CTAs of two; forward of
+  // 100000 x 1160: 95 us against 107)
+  if (s.W * 32 <= threads_sm / 2 && threads_sm / (s.W * 32) > resident * s.groups) {
+    s.groups = threads_sm / (s.W * 32);
+    s.threads = s.groups * s.W * 32;
+    resident = 1;
+  }
   const int64_t want = (rows + s.groups - 1) / s.groups;
   int64_t ctas = std::min<int64_t>(want, static_cast<int64_t>(SMS) * resident);
   // the groups' stride has to be a multiple of the period: fewer CTAs where all are resident, else more
@@ -754,9 +774,10 @@ Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_
 
 Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
   if (g.shifted() || H % 8) {
-    // Rows of partial granules, registers of 128 a thread with two vectors: two CTAs of up to 256 threads, rows of up
-    // to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps on the SM.
-    const int vecs = (H + (g.shifted() ? 7 : 0) + 7) / 8;
+    // Rows with elements outside their whole granules, registers of 128 a thread with two vectors: two CTAs of up to
+    // 256 threads, rows of up to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps
+    // on the SM (32768 x 5113: 297 us, against 374 with two vectors).
+    const int vecs = std::max(1, H / 8);  // whole granules of a row at most
     return shape_of(rows, H, g, vecs > 512 && vecs <= 640 ? 640 : 32, 512, 1, res ? 3 : 2);
   }
   // whole granules: 128 registers a thread, 512 threads an SM; or, rows of 4097 to 5120, two CTAs of up to 320 threads of
@@ -786,7 +807,7 @@ int wide_threads(int H) { return std::min(1024, std::max(32, (H + 127) / 128 * 3
 mt_status layernorm_fwd_launch(LnFwd a, cudaStream_t st) {
   Granules g(a.x, a.ld_x);
   g.add(a.y, a.ld_y);
-  if (!g.alike || a.H + (g.shifted() ? 7 : 0) > MAX_H_REG) {
+  if (!g.alike || a.H > MAX_H_REG) {
     const int64_t grid = std::min<int64_t>(a.rows, static_cast<int64_t>(num_sms()) * 2048 / wide_threads(a.H));
     layernorm_fwd_wide_kernel<<<static_cast<unsigned>(grid), wide_threads(a.H), 0, st>>>(a);
     return launch_check("layernorm_fwd_wide_kernel");
@@ -877,7 +898,7 @@ mt_status layernorm_bwd_launch(LnBwd a, cudaStream_t st) {
   g.add(a.dres, a.ld_dres);
   g.add(a.dx, a.ld_dx);
   int parts;
-  if (!g.alike || a.H + (g.shifted() ? 7 : 0) > MAX_H_REG) {
+  if (!g.alike || a.H > MAX_H_REG) {
     parts = static_cast<int>(std::min<int64_t>(2 * SMS, (a.rows + 63) / 64));
     if (a.dg || a.db) {
       layernorm_bwd_wide_cols_kernel<<<dim3((a.H + 255) / 256, parts), 256, 0, st>>>(a);

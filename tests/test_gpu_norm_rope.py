@@ -395,3 +395,54 @@ def test_mrope_of_very_wide_rows():
     torch.cuda.synchronize()
     ref, mag = _mrope_ref(H.host_f64(x), pos.cpu().numpy()[None], [1], heads, 2, 1e4, 0, 0, 0)
     _within(H.host_f64(y), ref, UB * np.abs(ref) + 10 * U * mag + 1e-38)
+
+
+@pytest.mark.parametrize("off", [0, 1, 3, 6, 7])
+@pytest.mark.parametrize("gap", [0, 1, 2, 4, 8])
+def test_layernorm_rows_around_one_granule(off, gap):
+    """Rows that start and end anywhere in their 16-byte granules: none, one or two whole ones, and elements before and
+    behind them."""
+    for width in (1, 2, 5, 7, 8, 9, 13, 15, 16, 17, 22, 31):
+        test_layernorm_forward(19, width, width + gap, off, True)
+        test_layernorm_backward(19, width, width + gap, off, True, True, None)
+
+
+# three warps a row: five groups to a CTA, every ring many times round
+@pytest.mark.parametrize("rows,width,ld,off", [(9000, 1152, 1152, 0), (9000, 1153, 1160, 0), (9000, 1401, 1401, 3), (8, 1536, 1536, 0),
+                                               (741, 1280, 1284, 0), (2960, 1031, 1031, 0)])
+def test_layernorm_of_three_warps_a_row(rows, width, ld, off):
+    test_layernorm_forward(rows, width, ld, off, True)
+    test_layernorm_backward(rows, width, ld, off, True, False, "dy")
+    test_layernorm_backward(rows, width, ld, off, True, True, None)
+
+
+@pytest.mark.parametrize("rows,width,ld,off", [(37, 9, 12, 1), (300, 257, 261, 0), (50, 1153, 1160, 0), (40, 4999, 5003, 5), (7, 8200, 8204, 0)])
+def test_layernorm_takes_nothing_from_between_the_rows(rows, width, ld, off):
+    """NaN between the rows and around them changes no bit of any result, and stays there."""
+    import torch
+    got = []
+    for fill in (7.0, float("nan")):
+        gen = torch.Generator().manual_seed(width)
+        def padded():
+            store = torch.full((off + rows * ld + 8,), fill, dtype=torch.bfloat16, device="cuda")
+            view = torch.as_strided(store, (rows, width), (ld, 1), off)
+            view.copy_(torch.randn(rows, width, generator=gen).cuda())
+            return view, store
+        x, _ = padded()
+        dy, _ = padded()
+        dres, _ = padded()
+        y, ys = padded()
+        dx, dxs = padded()
+        g = torch.randn(width, generator=gen).bfloat16().cuda()
+        mean, rstd, dg, db = H.empty_f32(rows), H.empty_f32(rows), H.empty_f32(width), H.empty_f32(width)
+        n = L.mt_layernorm_bwd_workspace_bytes(rows, width)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        L.mt_layernorm_fwd(x, ld, g, g, y, ld, mean, rstd, rows, width, EPS)
+        L.mt_layernorm_bwd(dy, ld, x, ld, g, mean, rstd, dres, ld, dx, ld, dg, db, rows, width, ws, n)
+        torch.cuda.synchronize()
+        for store in (ys, dxs):
+            outside = torch.ones(store.numel(), dtype=torch.bool, device="cuda")
+            torch.as_strided(outside, (rows, width), (ld, 1), off).fill_(False)
+            assert bool(torch.isnan(store[outside]).all()) if fill != fill else bool((store[outside] == fill).all())
+        got.append([t.clone() for t in (y, mean, rstd, dx, dg, db)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
