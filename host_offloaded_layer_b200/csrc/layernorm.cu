@@ -385,6 +385,19 @@ __device__ __forceinline__ void leave_sums(const LnBwd& a, const Cols<NV, EDGE>&
   }
 }
 
+// The same with the thread's places worked out anew, rather than kept in registers over the rows (32768 x 5120, one row
+// at a time: 177 us against 199, which spilled a register; with two rows at a time the registers are better used than
+// freed, 32768 x 3584: 123 us against 133).
+template <int NV, bool EDGE>
+__device__ __forceinline__ void leave_sums_anew(const LnBwd& a, float* sums, const f2 (&dg)[NV][4], const f2 (&db)[NV][4],
+                                                float edge_dg, float edge_db) {
+  int tid;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+  const int T = a.W * 32, group = tid / T, groups = blockDim.x / T;
+  const int shift = EDGE ? row_shift(a.x, a.ld_x, static_cast<int64_t>(blockIdx.x) * groups + group) : 0;
+  leave_sums<NV, EDGE>(a, Cols<NV, EDGE>(tid - group * T, T, shift, a.H), sums, group, groups, dg, db, edge_dg, edge_db);
+}
+
 // A row at a time, the next ones in flight.
 template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __grid_constant__ LnBwd a) {
@@ -516,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  leave_sums<NV, EDGE>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db, edge_dg, edge_db);
+  leave_sums_anew<NV, EDGE>(a, reinterpret_cast<float*>(smem), dg, db, edge_dg, edge_db);
 }
 
 // Rows of whole granules: R rows of a group at a time, through a ring of `slots` rows (a multiple of R, 2 R at least:
@@ -654,7 +667,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
     }
   }
   __syncthreads();
-  leave_sums<NV, false>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db, 0.f, 0.f);
+  if constexpr (R == 1)
+    leave_sums_anew<NV, false>(a, reinterpret_cast<float*>(smem), dg, db, 0.f, 0.f);
+  else
+    leave_sums<NV, false>(a, cols, reinterpret_cast<float*>(smem), group, groups, dg, db, 0.f, 0.f);
 }
 
 // dg and db from `parts` partial rows of 2H floats: 32 columns a block, 32 threads a column, each the sum of
@@ -776,12 +792,12 @@ Shape bwd_shape(int64_t rows, int H, const Granules& g, bool res) {
   if (g.shifted() || H % 8) {
     // Rows with elements outside their whole granules, registers of 128 a thread with two vectors: two CTAs of up to
     // 256 threads, rows of up to 4096. Up to 5120, one vector a thread and 640 threads of 96 registers keep more warps
-    // on the SM (32768 x 5113: 297 us, against 374 with two vectors).
+    // on the SM (32768 x 5113: 279 us, against 374 with two vectors).
     const int vecs = std::max(1, H / 8);  // whole granules of a row at most
     return shape_of(rows, H, g, vecs > 512 && vecs <= 640 ? 640 : 32, 512, 1, res ? 3 : 2);
   }
   // whole granules: 128 registers a thread, 512 threads an SM; or, rows of 4097 to 5120, two CTAs of up to 320 threads of
-  // 96 (32768 x 5120: 188 us, against 204 with one CTA of 128)
+  // 96 (32768 x 5120: 177 us, against 204 with one CTA of 128)
   const Shape s = shape_of(rows, H, g, 32, 512, 1, res ? 3 : 2);
   return s.threads > 256 && s.threads <= 320 ? shape_of(rows, H, g, 32, 640, 1, res ? 3 : 2) : s;
 }
@@ -871,7 +887,7 @@ mt_status bwd_bulk_go(LnBwd a, const Shape& s, cudaStream_t st) {
   const int64_t slot = static_cast<int64_t>(s.threads) * NV * 16 * (RES ? 3 : 2);
   const int resident = std::max(1, std::min(CTAS * THREADS / s.threads, 8));
   const int fit = static_cast<int>(std::min<int64_t>(MAX_SLOTS, (220 * 1024 / resident - 2048) / slot));
-  if constexpr (NV == 2 && THREADS == 320) {  // two rows' values do not fit its registers: 188 us one at a time, 198 two
+  if constexpr (NV == 2 && THREADS == 320) {  // two rows' values do not fit its registers: 177 us one at a time, 198 two
     a.slots = std::max(2, fit);
     return bwd_bulk_rows_go<NV, 1, RES, THREADS, CTAS>(a, s, slot, st);
   } else {
