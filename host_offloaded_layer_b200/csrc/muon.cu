@@ -1132,7 +1132,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   __syncthreads();
   fence_after();
   sm.tmem = *tmem_slot;
-  wait_for_last();
   if (a.vec4)
     scale_pass<4>(a.grad, a.walk, a.part, a.parts, a.eps, a.hi[0], a.two_term > 0 ? a.lo : nullptr, a.ld_x);
   else
