@@ -158,7 +158,7 @@ struct LnFwd {
 // R rows at a time: one exchange of R sums serves them. Two, where registers allow; rows of 4097 to 5120 would leave
 // one CTA of 320 threads on an SM then, so they go one at a time in two (32768 x 5120: 124 us, against 142 with one
 // vector a thread and 640 threads). A ring that bulk copies fill, as the backward's, was slower here (98304 x 3584:
-// 249 us against 231).
+// 249 us against 227).
 template <int NV, int R, bool EDGE, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __grid_constant__ LnFwd a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -398,8 +398,8 @@ __device__ __forceinline__ void leave_sums_anew(const LnBwd& a, float* sums, con
   leave_sums<NV, EDGE>(a, Cols<NV, EDGE>(tid - group * T, T, shift, a.H), sums, group, groups, dg, db, edge_dg, edge_db);
 }
 
-// A row at a time, the next ones in flight.
-template <int NV, bool EDGE, bool RES, int THREADS, int CTAS>
+// Rows with elements outside their whole granules: a row at a time, the next ones in flight.
+template <int NV, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __grid_constant__ LnBwd a) {
   constexpr int TENSORS = RES ? 3 : 2;
   extern __shared__ __align__(16) uint8_t smem[];  // the groups' rings; [groups][2][H] sums after the rows
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
   const int group = warp / W, wig = warp - group * W, groups = blockDim.x / T;
   const int t = threadIdx.x - group * T;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const Cols<NV, EDGE> cols(t, T, row_shift(a.x, a.ld_x, first), a.H);
+  const Cols<NV, true> cols(t, T, row_shift(a.x, a.ld_x, first), a.H);
   const uint32_t slice = static_cast<uint32_t>(T) * NV * 16;  // one row of one operand
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + group * (DEPTH * TENSORS * slice) + t * 16;
   const uint32_t ring_end = ring + DEPTH * TENSORS * slice;
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  leave_sums_anew<NV, EDGE>(a, reinterpret_cast<float*>(smem), dg, db, edge_dg, edge_db);
+  leave_sums_anew<NV, true>(a, reinterpret_cast<float*>(smem), dg, db, edge_dg, edge_db);
 }
 
 // Rows of whole granules: R rows of a group at a time, through a ring of `slots` rows (a multiple of R, 2 R at least:
@@ -777,13 +777,12 @@ Shape shape_of(int64_t rows, int H, const Granules& g, int one_vec, int threads_
     resident = 1;
   }
   const int64_t want = (rows + s.groups - 1) / s.groups;
-  int64_t ctas = std::min<int64_t>(want, static_cast<int64_t>(SMS) * resident);
-  // the groups' stride has to be a multiple of the period: fewer CTAs where all are resident, else more
-  if (ctas == static_cast<int64_t>(SMS) * resident)
-    while (ctas * s.groups % g.period()) --ctas;
-  else
-    while (ctas * s.groups % g.period()) ++ctas;
-  s.ctas = static_cast<int>(ctas);
+  const int64_t most = static_cast<int64_t>(SMS) * resident;
+  int64_t ctas = std::min(want, most), up = ctas;
+  // the groups' stride has to be a multiple of the period: more CTAs, or fewer where more would not be resident
+  while (up * s.groups % g.period()) ++up;
+  while (up > most && ctas * s.groups % g.period()) --ctas;
+  s.ctas = static_cast<int>(up > most ? ctas : up);
   s.smem = static_cast<int64_t>(s.threads) * s.nv * 16 * rows_stage * tensors * DEPTH;
   return s;
 }
@@ -865,7 +864,7 @@ mt_status bwd_launch(Kernel* kernel, SmemOptIn& opt, const LnBwd& a, const Shape
 template <int NV, bool RES, int THREADS, int CTAS>
 mt_status bwd_go(const LnBwd& a, const Shape& s, cudaStream_t st) {
   static SmemOptIn opt;
-  return bwd_launch(layernorm_bwd_kernel<NV, true, RES, THREADS, CTAS>, opt, a, s, s.smem, st);
+  return bwd_launch(layernorm_bwd_kernel<NV, RES, THREADS, CTAS>, opt, a, s, s.smem, st);
 }
 
 template <bool RES>
