@@ -1244,18 +1244,18 @@ struct TinyArgs {
   int steps;
   float scale;
   double eps;
-  double* gram;   // [parts][m * m]
+  double* gram;   // [parts][m * m]; the first becomes their sum, and then r
   int parts;
-  float* r;       // [m * m]
   __nv_bfloat16* o;
   int64_t ld_o;
 };
 
 constexpr int CHUNK = 64;  // long-side elements a CTA holds at a time
 
-// u[k][i] of a chunk from k0 into shared memory; first: also writes m'. A thread's 16 elements are in flight together.
+// u[k][i] p1 p2 of a chunk from k0 into shared memory; first: also writes m'. A thread's 16 elements are in flight
+// together.
 template <class T, int LD>
-__device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)[LD], bool first) {
+__device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)[LD], bool first, float p1 = 1.f, float p2 = 1.f) {
   constexpr int N = CHUNK * TINY / 256;
   const int kn = static_cast<int>(min(static_cast<int64_t>(CHUNK), a.n - k0));
   const bool want_g = !a.p.m_in || first || a.p.nesterov;
@@ -1284,7 +1284,7 @@ __device__ __forceinline__ void tiny_chunk(const TinyArgs& a, int64_t k0, T (*u)
         v = a.p.nesterov ? fmaf(a.p.mu, vm[q], v) : vm[q];
       }
     }
-    u[k][i] = static_cast<T>(v);
+    u[k][i] = static_cast<T>(first ? v : v * p1 * p2);
   }
 }
 
@@ -1396,7 +1396,8 @@ constexpr int TINY_SMEM = (6 * TINY * TINY + 4 * TINY_ROWS * TINY) * 4;
 
 // The steps on the Gram matrix, eight CTAs of a cluster with eight rows each: with P = a I + b A + c A^2,
 // Q <- P Q, A <- A P^2. A product writes no matrix that it reads, and a cluster barrier stands behind each.
-// r = scale * Q / (|u| + eps).
+// r = Q / (|u| + eps) in fp64 (its elements leave fp32 for norms below 1e-36 with an eps as small), over the Gram
+// matrix, which every CTA has read by then.
 __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_tiny_steps_kernel(TinyArgs a) {
   extern __shared__ __align__(16) float tiny_smem[];
   Mat64 A = reinterpret_cast<Mat64>(tiny_smem), A_next = A + TINY, P = A + 2 * TINY, P2 = A + 3 * TINY, Q = A + 4 * TINY,
@@ -1445,27 +1446,33 @@ __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_ti
     A = A_next;
     A_next = t;
   }
-  const double f = a.scale * inv;
 #pragma unroll
   for (int q = 0; q < 2; ++q)
-    if (own_row < a.m && own_col + q < a.m) a.r[own_row * a.m + own_col + q] = static_cast<float>(Q[own_row][own_col + q] * f);
+    if (own_row < a.m && own_col + q < a.m) a.gram[own_row * a.m + own_col + q] = Q[own_row][own_col + q] * inv;
 }
 
-// o = r u, a chunk of the long side a CTA. Rows of 68 in shared memory: four j a read, no bank conflicts.
+// o = scale r u, a chunk of the long side a CTA: (r 2^-e) (u 2^e) with 2^e about an element of r's diagonal, which is
+// positive and within a factor of a^steps of the others, so that both stay in fp32's range for any norm and eps. Rows
+// of 68 in shared memory: four j a read, no bank conflicts.
 constexpr int APPLY_LD = TINY + 4;
 __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   __shared__ __align__(16) float u[CHUNK][APPLY_LD];
   __shared__ __align__(16) float r[TINY][APPLY_LD];
   wait_for_last();
+  const double lead = a.gram[0];
+  const int e = lead > 0.0 && isfinite(lead) ? ilogb(lead) : 0;
+  const float p1 = ldexpf(1.f, e / 2), p2 = ldexpf(1.f, e - e / 2);  // 2^e may leave fp32 itself
   {
-    float v[TINY * TINY / 256];
+    double v[TINY * TINY / 256];
 #pragma unroll
     for (int q = 0; q < TINY * TINY / 256; ++q) {
       const int i = (threadIdx.x + q * 256) / TINY, j = threadIdx.x % TINY;
-      v[q] = i < a.m && j < a.m ? a.r[i * a.m + j] : 0.f;
+      v[q] = i < a.m && j < a.m ? a.gram[i * a.m + j] : 0.0;
     }
+    const double down = ldexp(1.0, -e);
 #pragma unroll
-    for (int q = 0; q < TINY * TINY / 256; ++q) r[(threadIdx.x + q * 256) / TINY][threadIdx.x % TINY] = v[q];
+    for (int q = 0; q < TINY * TINY / 256; ++q)
+      r[(threadIdx.x + q * 256) / TINY][threadIdx.x % TINY] = static_cast<float>(v[q] * down);
   }
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
   // neighbouring threads write neighbouring elements of a row of o: along the short side of a tall matrix, the long
@@ -1473,7 +1480,7 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   const int fast = threadIdx.x & 63, slow = threadIdx.x >> 6;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk<float, APPLY_LD>(a, c * CHUNK, u, false);
+    tiny_chunk<float, APPLY_LD>(a, c * CHUNK, u, false, p1, p2);
     __syncthreads();
     float s[16] = {};
     const float(*mine)[APPLY_LD] = a.tall ? r : u, (*other)[APPLY_LD] = a.tall ? u : r;
@@ -1493,7 +1500,7 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
       const int k = a.tall ? slow + 4 * q : fast, i = a.tall ? fast : slow + 4 * q;
       const int64_t lk = c * CHUNK + k;
       if (lk < a.n && i < a.m)
-        a.o[a.tall ? lk * a.ld_o + i : static_cast<int64_t>(i) * a.ld_o + lk] = __float2bfloat16_rn(s[q]);
+        a.o[a.tall ? lk * a.ld_o + i : static_cast<int64_t>(i) * a.ld_o + lk] = __float2bfloat16_rn(s[q] * a.scale);
     }
   }
 }
@@ -1508,7 +1515,6 @@ struct Plan {
   float* partial;  // and their parts
   __half *hi[2], *lo, *A, *P, *C;  // C: only where the first two steps share a Gram matrix
   double* gram;
-  float* r;
   uint64_t bytes;
 };
 
@@ -1540,7 +1546,6 @@ Plan plan(int64_t rows, int64_t cols, void* ws) {
   if (p.m <= TINY) {
     p.parts = static_cast<int>(std::min<int64_t>(148, (p.n + CHUNK - 1) / CHUNK));
     p.gram = b.take<double>(static_cast<int64_t>(p.parts) * p.m * p.m);
-    p.r = b.take<float>(p.m * p.m);
   } else {
     p.parts = NORM_PARTS;
     p.ld_x = align_up(cols, 64);
@@ -1584,7 +1589,6 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
   a.eps = c.eps;
   a.gram = p.gram;
   a.parts = p.parts;
-  a.r = p.r;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
   muon_tiny_gram_kernel<<<p.parts, 256, 0, st>>>(a);
