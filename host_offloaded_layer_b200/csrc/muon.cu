@@ -196,7 +196,7 @@ __device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const d
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float u = !p.m_in ? g[k][i] : p.nesterov ? fmaf(p.mu, m[k][i], g[k][i]) : m[k][i];
-          const float v = u * mant * p1 * p2;
+          const float v = u * p1 * mant * p2;  // a subnormal u is lifted before the factor that rounds
           h[i] = __float2half_rn(v);
           l[i] = __float2half_rn(v - __half2float(h[i]));
         }

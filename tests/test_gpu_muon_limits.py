@@ -51,3 +51,17 @@ def test_short_sides_of_zeros_and_tiny_norms_with_an_eps_as_tiny(rows, cols):
             g = (torch.randn(rows, cols, generator=gen, dtype=torch.float64) * size).float().cuda()
             ref = _exact(g.double(), cfg.steps, cfg.eps)
             assert (_update(g, cfg) - ref).norm() <= (1.01 * UB + 2.0 ** -12) * ref.norm(), (eps, size)
+
+
+@pytest.mark.parametrize("rows,cols", [(250, 500), (500, 250), (1200, 1300)])
+def test_subnormal_gradients_lose_no_bits(rows, cols):
+    """u / |u| of a gradient made of 2^-149 times small whole numbers is that of the whole numbers: scaling by a power of
+    two changes no rounding where neither side is subnormal on the way, so the two results are equal bit for bit."""
+    import torch
+    gen = torch.Generator().manual_seed(rows)
+    whole = torch.randint(-7, 8, (rows, cols), generator=gen).double()
+    cfg = L.make_muon_cfg(eps=1e-45)  # 2^-149, against norms of a thousand times that
+    tiny = (whole * 2.0 ** -149).float().cuda()
+    assert bool((tiny.double() == (whole * 2.0 ** -149).cuda()).all())
+    cfg1 = L.make_muon_cfg(eps=1.0)
+    assert torch.equal(_update(tiny, cfg), _update(whole.float().cuda(), cfg1))
