@@ -22,7 +22,8 @@
 // |u|_F is summed in fp64, so that no magnitude of g that fp32 holds over- or underflows.
 //
 // Matrices whose short side is at most 64 take no tensor cores: their Gram matrix (in fp64) is all that the
-// steps need, one cluster runs them on it in fp32, and the result is one product with u: four launches.
+// steps need, one cluster runs them on it (up to five in fp32, more in fp64), and the result is one product with u: four
+// launches.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -38,6 +39,7 @@ namespace {
 using namespace tc;
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
+constexpr double NS64_A = 3.4445, NS64_B = -4.7750, NS64_C = 2.0315;
 constexpr float S_X = 16384.f, S_A = 16384.f, S_P = 8192.f;
 constexpr int64_t MAX_ELEMENTS = 1ll << 36;  // no device holds more; sizes and tile numbers stay in range
 constexpr int TINY = 64;  // the widest short side of the Gram path
@@ -1243,7 +1245,7 @@ struct TinyArgs {
   int tall;    // rows are the long side
   int steps;
   float scale;
-  double eps;
+  double eps, floor;  // floor: added to the diagonal of X X^T in fp64
   double* gram;   // [parts][m * m]; the first becomes their sum, and then r
   int parts;
   __nv_bfloat16* o;
@@ -1343,66 +1345,116 @@ __global__ void __launch_bounds__(256) muon_tiny_reduce_kernel(TinyArgs a) {
   }
 }
 
-using Mat64 = float (*)[TINY];
+// What the steps and the product behind them compute in: T = float or double, 16 bytes of either, and two of them.
+template <class T>
+struct TinyNum;
+template <>
+struct TinyNum<float> {
+  using pair = float2;
+  static constexpr float A = NS_A, B = NS_B, C = NS_C;
+};
+template <>
+struct TinyNum<double> {
+  using pair = double2;
+  static constexpr double A = NS64_A, B = NS64_B, C = NS64_C;
+};
+template <class T>
+struct __align__(16) Vec16 {
+  static constexpr int N = 16 / sizeof(T);
+  T v[N];
+};
+template <class T>
+__device__ __forceinline__ Vec16<T> ld16(const T* p) {
+  return *reinterpret_cast<const Vec16<T>*>(p);
+}
+__device__ __forceinline__ void st_pair(uint32_t at, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_pair(uint32_t at, double2 v) {
+  asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(at), "d"(v.x), "d"(v.y) : "memory");
+}
+
+template <class T>
+using Mat64 = T (*)[TINY];
 constexpr int TINY_CTAS = 8, TINY_ROWS = TINY / TINY_CTAS;  // the steps' cluster, and the rows of each product that a CTA computes
 
 // This CTA's rows of s * a b, 64 x 64 matrices that every CTA of the cluster holds whole: thread (q, r, c) sums a
-// quarter of k for 2 rows x 4 columns, the quarters meet in `part`, and thread t gets elements 2t, 2t + 1 of the
-// CTA's 8 x 64. (Operands are symmetric but for rounding; reading a by columns would let that difference grow from
-// step to step.)
-__device__ __forceinline__ float2 mul64(Mat64 a, Mat64 b, int rank, float (*part)[TINY_ROWS * TINY]) {
+// quarter of k for 2 rows x 4 columns (one vector of 16 bytes, or two half a row apart: neighbouring threads read
+// neighbouring vectors), the quarters meet in `part`, and thread t gets elements 2t, 2t + 1 of the CTA's 8 x 64.
+// (Operands are symmetric but for rounding; reading a by columns would let that difference grow from step to step.)
+template <class T>
+__device__ __forceinline__ typename TinyNum<T>::pair mul64(Mat64<T> a, Mat64<T> b, int rank, T (*part)[TINY_ROWS * TINY]) {
+  constexpr int E = Vec16<T>::N, H = 4 / E;
   const int c = threadIdx.x & 15, r = (threadIdx.x >> 4) & 3, q = threadIdx.x >> 6, row = rank * TINY_ROWS + 2 * r;
-  float acc[2][4] = {};
+  T acc[2][4] = {};
 #pragma unroll
-  for (int k = q * 16; k < q * 16 + 16; k += 4) {
-    float4 x[2], y[4];
+  for (int k = q * 16; k < q * 16 + 16; k += E) {
+    Vec16<T> x[2], y[E][H];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const float4*>(&a[row + i][k]);
+    for (int i = 0; i < 2; ++i) x[i] = ld16<T>(&a[row + i][k]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4*>(&b[k + i][c * 4]);
+    for (int l = 0; l < E; ++l)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      for (int h = 0; h < H; ++h) y[l][h] = ld16<T>(&b[k + l][32 * h + E * c]);
 #pragma unroll
-      for (int l = 0; l < 4; ++l) {
-        acc[i][0] = fmaf(xs[l], y[l].x, acc[i][0]);
-        acc[i][1] = fmaf(xs[l], y[l].y, acc[i][1]);
-        acc[i][2] = fmaf(xs[l], y[l].z, acc[i][2]);
-        acc[i][3] = fmaf(xs[l], y[l].w, acc[i][3]);
-      }
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int l = 0; l < E; ++l)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int j = 0; j < E; ++j) acc[i][E * h + j] = fma(x[i].v[l], y[l][h].v[j], acc[i][E * h + j]);
   }
   __syncthreads();  // `part` of the product before is read
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    *reinterpret_cast<float4*>(&part[q][(2 * r + i) * TINY + c * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-  __syncthreads();
-  float2 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float2*>(&part[i][2 * threadIdx.x]);
-  return make_float2(v[0].x + v[1].x + (v[2].x + v[3].x), v[0].y + v[1].y + (v[2].y + v[3].y));
+    for (int h = 0; h < H; ++h) {
+      Vec16<T> w;
+#pragma unroll
+      for (int j = 0; j < E; ++j) w.v[j] = acc[i][E * h + j];
+      *reinterpret_cast<Vec16<T>*>(&part[q][(2 * r + i) * TINY + 32 * h + E * c]) = w;
+    }
+  __syncthreads();
+  typename TinyNum<T>::pair v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const typename TinyNum<T>::pair*>(&part[i][2 * threadIdx.x]);
+  v[0].x = v[0].x + v[1].x + (v[2].x + v[3].x);
+  v[0].y = v[0].y + v[1].y + (v[2].y + v[3].y);
+  return v[0];
 }
 
 // Elements 2t, 2t + 1 of this CTA's rows of c, to every CTA of the cluster.
-__device__ __forceinline__ void share64(Mat64 c, int rank, float2 v) {
-  const uint32_t at = smem_u32(&c[rank * TINY_ROWS][0]) + threadIdx.x * 8;
+template <class T>
+__device__ __forceinline__ void share64(Mat64<T> c, int rank, typename TinyNum<T>::pair v) {
+  const uint32_t at = smem_u32(&c[rank * TINY_ROWS][0]) + threadIdx.x * sizeof(v);
 #pragma unroll
-  for (int p = 0; p < TINY_CTAS; ++p)
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_to_rank(at, static_cast<uint32_t>(p))), "f"(v.x), "f"(v.y)
-                 : "memory");
+  for (int p = 0; p < TINY_CTAS; ++p) st_pair(map_to_rank(at, static_cast<uint32_t>(p)), v);
 }
 
-constexpr int TINY_SMEM = (6 * TINY * TINY + 4 * TINY_ROWS * TINY) * 4;
+template <class T>
+constexpr int TINY_SMEM = (6 * TINY * TINY + 4 * TINY_ROWS * TINY) * sizeof(T);
 
 // The steps on the Gram matrix, eight CTAs of a cluster with eight rows each: with P = a I + b A + c A^2,
 // Q <- P Q, A <- A P^2. A product writes no matrix that it reads, and a cluster barrier stands behind each.
 // r = Q / (|u| + eps) in fp64 (its elements leave fp32 for norms below 1e-36 with an eps as small), over the Gram
 // matrix, which every CTA has read by then.
+//
+// A is never formed anew from X: what rounding leaves in directions that u lacks, of either sign, grows by a^2 = 11.9 a
+// step, and the polynomial of a negative eigenvalue that has grown to about one only grows. In fp32 five steps stay
+// within 7e-4 of exact ones (48 equal rows; 2e-4 for rank one over noise of 1e-3), six within 3e-3, eight are off by
+// the result itself. More than five are therefore taken in fp64, and A starts with `floor` added to its diagonal, more
+// than what the roundings of the Gram sums and of a step can take off (a sum's chain of additions, and 512, times 2^-53:
+// the rows' absolute products have a 2-norm of at most |X|_F^2 = 1). No eigenvalue turns negative then, for any number of
+// steps: the result is q(A) u, the exact steps but in directions weaker than sqrt(floor), some 2^-22 of |u|, which
+// come out weaker than exact steps have them after a dozen. 60 x 20000, ten steps: 127 us, 84 in fp32.
+template <class T>
 __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_tiny_steps_kernel(TinyArgs a) {
-  extern __shared__ __align__(16) float tiny_smem[];
-  Mat64 A = reinterpret_cast<Mat64>(tiny_smem), A_next = A + TINY, P = A + 2 * TINY, P2 = A + 3 * TINY, Q = A + 4 * TINY,
-        Q_next = A + 5 * TINY;
-  float(*part)[TINY_ROWS * TINY] = reinterpret_cast<float(*)[TINY_ROWS * TINY]>(A + 6 * TINY);
+  using Num = TinyNum<T>;
+  extern __shared__ __align__(16) uint8_t tiny_smem[];
+  Mat64<T> A = reinterpret_cast<Mat64<T>>(tiny_smem), A_next = A + TINY, P = A + 2 * TINY, P2 = A + 3 * TINY, Q = A + 4 * TINY,
+           Q_next = A + 5 * TINY;
+  T(*part)[TINY_ROWS * TINY] = reinterpret_cast<T(*)[TINY_ROWS * TINY]>(A + 6 * TINY);
   __shared__ double trace[TINY];
   const int rank = static_cast<int>(cluster_rank());
   release_next();
@@ -1421,25 +1473,26 @@ __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_ti
 #pragma unroll
   for (int q = 0; q < TINY * TINY / 256; ++q) {
     const int e = threadIdx.x + q * 256;
-    A[e / TINY][e % TINY] = static_cast<float>(own[q] * inv * inv);
-    Q[e / TINY][e % TINY] = e / TINY == e % TINY ? 1.f : 0.f;
+    const bool diag = e / TINY == e % TINY;
+    A[e / TINY][e % TINY] = static_cast<T>(own[q] * inv * inv + (sizeof(T) == 8 && diag ? a.floor : 0.0));
+    Q[e / TINY][e % TINY] = diag ? T(1) : T(0);
   }
   cluster_sync();  // every CTA has started, and holds A
   const int own_row = rank * TINY_ROWS + (threadIdx.x >> 5), own_col = 2 * (threadIdx.x & 31);
   for (int st = 0; st < a.steps; ++st) {
-    float2 v = mul64(A, A, rank, part);
-    v.x = fmaf(NS_C, v.x, fmaf(NS_B, A[own_row][own_col], own_row == own_col ? NS_A : 0.f));
-    v.y = fmaf(NS_C, v.y, fmaf(NS_B, A[own_row][own_col + 1], own_row == own_col + 1 ? NS_A : 0.f));
-    share64(P, rank, v);
+    typename Num::pair v = mul64<T>(A, A, rank, part);
+    v.x = fma(Num::C, v.x, fma(Num::B, A[own_row][own_col], own_row == own_col ? Num::A : T(0)));
+    v.y = fma(Num::C, v.y, fma(Num::B, A[own_row][own_col + 1], own_row == own_col + 1 ? Num::A : T(0)));
+    share64<T>(P, rank, v);
     cluster_sync();
-    share64(Q_next, rank, mul64(P, Q, rank, part));
+    share64<T>(Q_next, rank, mul64<T>(P, Q, rank, part));
     if (st + 1 < a.steps) {
-      share64(P2, rank, mul64(P, P, rank, part));
+      share64<T>(P2, rank, mul64<T>(P, P, rank, part));
       cluster_sync();
-      share64(A_next, rank, mul64(A, P2, rank, part));
+      share64<T>(A_next, rank, mul64<T>(A, P2, rank, part));
     }
     cluster_sync();
-    Mat64 t = Q;
+    Mat64<T> t = Q;
     Q = Q_next;
     Q_next = t;
     t = A;
@@ -1451,16 +1504,22 @@ __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_ti
     if (own_row < a.m && own_col + q < a.m) a.gram[own_row * a.m + own_col + q] = Q[own_row][own_col + q] * inv;
 }
 
-// o = scale r u, a chunk of the long side a CTA: (r 2^-e) (u 2^e) with 2^e about an element of r's diagonal, which is
-// positive and within a factor of a^steps of the others, so that both stay in fp32's range for any norm and eps. Rows
-// of 68 in shared memory: four j a read, no bank conflicts.
-constexpr int APPLY_LD = TINY + 4;
+// o = scale r u, a chunk of the long side a CTA. In fp32, (r 2^-e) (u 2^e) with 2^e about an element of r's diagonal,
+// which is positive and within a factor of a^steps of the others, so that both stay in range for any norm and eps. After
+// more than five steps in fp64, as r's elements grow by a with each and cancel in strong directions (60 x 20000: 7 us
+// more). Rows of 16 bytes more than 64 elements in shared memory: a vector of j a read, no bank conflicts.
+template <class T>
+constexpr int APPLY_LD = TINY + Vec16<T>::N;
+template <class T>
+constexpr int APPLY_SMEM = (CHUNK + TINY) * APPLY_LD<T> * sizeof(T);
+template <class T>
 __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
-  __shared__ __align__(16) float u[CHUNK][APPLY_LD];
-  __shared__ __align__(16) float r[TINY][APPLY_LD];
+  constexpr int LD = APPLY_LD<T>, E = Vec16<T>::N;
+  extern __shared__ __align__(16) uint8_t apply_smem[];
+  T(*u)[LD] = reinterpret_cast<T(*)[LD]>(apply_smem), (*r)[LD] = u + CHUNK;
   wait_for_last();
   const double lead = a.gram[0];
-  const int e = lead > 0.0 && isfinite(lead) ? ilogb(lead) : 0;
+  const int e = sizeof(T) == 4 && lead > 0.0 && isfinite(lead) ? ilogb(lead) : 0;
   const float p1 = ldexpf(1.f, e / 2), p2 = ldexpf(1.f, e - e / 2);  // 2^e may leave fp32 itself
   {
     double v[TINY * TINY / 256];
@@ -1472,7 +1531,7 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
     const double down = ldexp(1.0, -e);
 #pragma unroll
     for (int q = 0; q < TINY * TINY / 256; ++q)
-      r[(threadIdx.x + q * 256) / TINY][threadIdx.x % TINY] = static_cast<float>(v[q] * down);
+      r[(threadIdx.x + q * 256) / TINY][threadIdx.x % TINY] = static_cast<T>(v[q] * down);
   }
   const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
   // neighbouring threads write neighbouring elements of a row of o: along the short side of a tall matrix, the long
@@ -1480,19 +1539,17 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
   const int fast = threadIdx.x & 63, slow = threadIdx.x >> 6;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     __syncthreads();
-    tiny_chunk<float, APPLY_LD>(a, c * CHUNK, u, false, p1, p2);
+    tiny_chunk<T, LD>(a, c * CHUNK, u, false, p1, p2);
     __syncthreads();
-    float s[16] = {};
-    const float(*mine)[APPLY_LD] = a.tall ? r : u, (*other)[APPLY_LD] = a.tall ? u : r;
-    for (int j = 0; j < a.m; j += 4) {  // zeros behind a.m
-      const float4 x = *reinterpret_cast<const float4*>(&mine[fast][j]);
+    T s[16] = {};
+    const T(*mine)[LD] = a.tall ? r : u, (*other)[LD] = a.tall ? u : r;
+    for (int j = 0; j < a.m; j += E) {  // zeros behind a.m
+      const Vec16<T> x = ld16<T>(&mine[fast][j]);
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        const float4 y = *reinterpret_cast<const float4*>(&other[slow + 4 * q][j]);
-        s[q] = fmaf(x.x, y.x, s[q]);
-        s[q] = fmaf(x.y, y.y, s[q]);
-        s[q] = fmaf(x.z, y.z, s[q]);
-        s[q] = fmaf(x.w, y.w, s[q]);
+        const Vec16<T> y = ld16<T>(&other[slow + 4 * q][j]);
+#pragma unroll
+        for (int l = 0; l < E; ++l) s[q] = fma(x.v[l], y.v[l], s[q]);
       }
     }
 #pragma unroll
@@ -1500,7 +1557,7 @@ __global__ void __launch_bounds__(256) muon_tiny_apply_kernel(TinyArgs a) {
       const int k = a.tall ? slow + 4 * q : fast, i = a.tall ? fast : slow + 4 * q;
       const int64_t lk = c * CHUNK + k;
       if (lk < a.n && i < a.m)
-        a.o[a.tall ? lk * a.ld_o + i : static_cast<int64_t>(i) * a.ld_o + lk] = __float2bfloat16_rn(s[q] * a.scale);
+        a.o[a.tall ? lk * a.ld_o + i : static_cast<int64_t>(i) * a.ld_o + lk] = __float2bfloat16_rn(static_cast<float>(s[q] * a.scale));
     }
   }
 }
@@ -1578,6 +1635,18 @@ Walk make_walk(int64_t rows, int64_t cols, int vec) {
   return w;
 }
 
+// The steps on the Gram matrix, and the product behind them.
+template <class T>
+mt_status muon_tiny_rest(const TinyArgs& a, cudaStream_t st) {
+  static SmemOptIn opt_steps, opt_apply;
+  MT_TRY(opt_steps.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel<T>), TINY_SMEM<T>));
+  MT_TRY(opt_apply.raise(reinterpret_cast<const void*>(muon_tiny_apply_kernel<T>), APPLY_SMEM<T>));
+  MT_TRY(launch_ahead(muon_tiny_steps_kernel<T>, "muon_tiny_steps_kernel", TINY_CTAS, 256, TINY_SMEM<T>, 0, st, a));
+  const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
+  return launch_ahead(muon_tiny_apply_kernel<T>, "muon_tiny_apply_kernel", static_cast<int>(std::min<int64_t>(chunks, 4 * num_sms())),
+                      256, APPLY_SMEM<T>, 0, st, a);
+}
+
 mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_o, const Plan& p, cudaStream_t st) {
   TinyArgs a;
   a.p = g;
@@ -1587,19 +1656,18 @@ mt_status muon_tiny(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t ld_
   a.steps = c.steps;
   a.scale = c.scale;
   a.eps = c.eps;
+  // a Gram sum's chain of additions: the elements of a CTA's chunks, then the parts
+  const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
+  const int64_t chain = (chunks + p.parts - 1) / p.parts * CHUNK + (p.parts + 7) / 8 + 8;
+  a.floor = std::ldexp(static_cast<double>(chain + 512), -53);
   a.gram = p.gram;
   a.parts = p.parts;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.ld_o = ld_o;
   muon_tiny_gram_kernel<<<p.parts, 256, 0, st>>>(a);
   MT_TRY(launch_check("muon_tiny_gram_kernel"));
-  static SmemOptIn opt;
-  MT_TRY(opt.raise(reinterpret_cast<const void*>(muon_tiny_steps_kernel)));
   MT_TRY(launch_ahead(muon_tiny_reduce_kernel, "muon_tiny_reduce_kernel", (a.m * a.m + 31) / 32, 256, 0, 0, st, a));
-  MT_TRY(launch_ahead(muon_tiny_steps_kernel, "muon_tiny_steps_kernel", TINY_CTAS, 256, TINY_SMEM, 0, st, a));
-  const int64_t chunks = (p.n + CHUNK - 1) / CHUNK;
-  return launch_ahead(muon_tiny_apply_kernel, "muon_tiny_apply_kernel", static_cast<int>(std::min<int64_t>(chunks, 4 * num_sms())),
-                      256, 0, 0, st, a);
+  return c.steps <= 5 ? muon_tiny_rest<float>(a, st) : muon_tiny_rest<double>(a, st);
 }
 
 template <bool TALL>

@@ -533,8 +533,9 @@ uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols);
  * buffer is then updated in place); both NULL: u = g. o: bf16, rows ld_o
  * elements apart, the direction to take off the weights. A matrix taller than
  * wide uses A = X^T X. The products run on the tensor cores in fp16 with fp32
- * sums (short sides of at most 64: fp32); before its rounding to bf16 the result
- * is within about 2e-3 (2-norm) of the same steps in fp64 for 5 steps. Elements
+ * sums (short sides of at most 64: fp32 up to 5 steps, fp64 beyond); before its
+ * rounding to bf16 the result is within about 2e-3 (2-norm) of the same steps in
+ * fp64 for 5 steps. Elements
  * between cols and a row's stride are neither read nor written. A g or m that
  * holds infinities or NaN gives NaN. Deterministic: fixed order of every sum.
  * g, m_in, m_out, o: aligned to their elements (16-byte aligned rows of 4

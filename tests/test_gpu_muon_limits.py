@@ -65,3 +65,80 @@ def test_subnormal_gradients_lose_no_bits(rows, cols):
     assert bool((tiny.double() == (whole * 2.0 ** -149).cuda()).all())
     cfg1 = L.make_muon_cfg(eps=1.0)
     assert torch.equal(_update(tiny, cfg), _update(whole.float().cuda(), cfg1))
+
+
+def _matrix(kind, rows, cols, seed):
+    """Gradients that lack directions. Those of whole numbers lack them exactly, in fp32 as in float64."""
+    gen = torch_generator(seed)
+    import torch
+    whole = lambda *s: torch.randint(-8, 9, s, generator=gen).double()  # noqa: E731
+    if kind == "rank 1":
+        g = whole(rows, 1) @ whole(1, cols)
+    elif kind == "rank 8":
+        g = whole(rows, 8) @ whole(8, cols)
+    elif kind == "equal":
+        g = torch.ones(rows, cols, dtype=torch.float64)
+    elif kind == "rows four times":
+        g = torch.randn((rows + 3) // 4, cols, generator=gen).double().repeat_interleave(4, 0)[:rows]
+    elif kind == "strong + 1e-3":
+        g = (torch.randn(rows, 1, generator=gen) @ torch.randn(1, cols, generator=gen)
+             + 1e-3 * torch.randn(rows, cols, generator=gen)).double()
+    else:
+        g = torch.randn(rows, cols, generator=gen).double()
+    return (g * 2.0 ** -10).float()
+
+
+def torch_generator(seed):
+    import torch
+    return torch.Generator().manual_seed(seed)
+
+
+def _after(s, steps):
+    """What `steps` steps make of singular values s, and |s f'/f|, how they pass on a relative change."""
+    d = s * 0 + 1
+    x = s.clone()
+    for _ in range(steps):
+        d = d * (NA + 3 * NB * x ** 2 + 5 * NC * x ** 4)
+        x = NA * x + NB * x ** 3 + NC * x ** 5
+    return x, (s * d / x).abs()
+
+
+KINDS = ["rank 1", "rank 8", "equal", "rows four times", "strong + 1e-3", "full"]
+
+
+@pytest.mark.parametrize("steps", [1, 5, 6, 7, 10, 12, 20])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(48, 2000), (2000, 48), (64, 64), (32, 500), (13, 70)])
+def test_short_sides_follow_the_exact_steps(rows, cols, kind, steps):
+    """Up to five steps the header's 2e-3 (2-norm); more run in fp64: each singular value's X X^T is off by at most
+    2^-53 times 512 and the longest chain of additions (what is added to the diagonal), relative to s^2 half of that,
+    and a step's products by 2^-53 times 64 terms a few times, below 2^-40 for all steps; the scalar map passes both on.
+    The reference has noise of its own in directions that u lacks: 2^-46 of |u| grown by 3.4445 a step."""
+    import torch
+    g = _matrix(kind, rows, cols, rows + steps).cuda()
+    cfg = L.make_muon_cfg(steps=steps)
+    ref = _exact(g.double(), steps, cfg.eps)
+    off = (_update(g, cfg) - ref).norm()
+    allowed = 1.01 * UB * ref.norm()
+    if steps <= 5:
+        allowed += 2e-3 * ref.norm()
+    else:
+        u = g.double().cpu()
+        s = torch.linalg.svdvals(u / (u.norm() + cfg.eps))
+        s = s[s > 1e-9]
+        x, pass_on = _after(s, steps)
+        n = max(rows, cols)
+        floor = (-(-n // 64 // 148) * 64 + 64 + 28 + 512) * 2.0 ** -53
+        allowed += (x * pass_on * (floor / (2 * s * s) + 2.0 ** -40)).norm() + 2.0 ** -46 * NA ** steps
+    assert off <= allowed, (float(off / ref.norm()), float(allowed / ref.norm()))
+
+
+@pytest.mark.parametrize("steps", [30, 100])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(48, 2000), (300, 64)])
+def test_short_sides_stay_bounded_for_any_number_of_steps(rows, cols, kind, steps):
+    """The polynomial maps [0, 1] into [0, 1.2024]: so do the steps on any matrix near u, and bf16 adds 2^-8 at most."""
+    import torch
+    o = _update(_matrix(kind, rows, cols, steps).cuda(), L.make_muon_cfg(steps=steps))
+    assert bool(torch.isfinite(o).all()) and float(torch.linalg.matrix_norm(o, 2)) <= 1.2024 * (1 + UB)
+    assert float(torch.linalg.matrix_norm(o, 2)) > 0.5  # nor does the strongest direction vanish
