@@ -473,16 +473,6 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
   return mbar_wait(bar, parity, abort_flag, err, code);
 }
 
-// After a wait ran out: the loads that this thread has issued into a ring of `stages` land before the CTA leaves
-// (each waited for at most a second, whatever the abort flag says).
-__device__ __forceinline__ void drain_ring(uint32_t full, uint32_t issued, uint32_t stages) {
-  for (uint32_t g = issued > stages ? issued - stages : 0; g < issued; ++g) {
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try(full + 8 * (g % stages), (g / stages) & 1u))
-      if (globaltimer() - t0 > 1000000000ull) break;
-  }
-}
-
 // Instruction descriptor of kind::f16 with fp16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |

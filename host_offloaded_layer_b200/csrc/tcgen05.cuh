@@ -66,6 +66,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// After a wait ran out: the loads that this thread has issued into a ring of `stages` (the g-th into stage g % stages)
+// land before the CTA leaves (each waited for at most a second, whatever the abort flag says).
+static __device__ void drain_ring(uint32_t full, uint32_t issued, uint32_t stages) {
+  for (uint32_t g = issued > stages ? issued - stages : 0; g < issued; ++g) {
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try(full + 8 * (g % stages), (g / stages) & 1u))
+      if (globaltimer() - t0 > 1000000000ull) break;
+  }
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
