@@ -693,10 +693,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
 }
 
 // dg and db from `parts` partial rows of 2H floats: 32 columns a block, 32 threads a column, each the sum of
-// every 32nd row, added in order. Launched ahead of the pass's end (its CTAs start as that one's leave).
+// every 32nd row, added in order. Launched ahead of the pass's end (its CTAs start as that one's leave): `part` is still written
+// then, so it is no const __restrict__, whose loads may go by the non-coherent path and ahead of the wait.
 constexpr int REDUCE_Y = 32;
-__global__ void __launch_bounds__(32 * REDUCE_Y) layernorm_bwd_reduce_kernel(const float* __restrict__ part, int parts, int H,
-                                                                             float* __restrict__ dg, float* __restrict__ db) {
+__global__ void __launch_bounds__(32 * REDUCE_Y) layernorm_bwd_reduce_kernel(const float* part, int parts, int H, float* dg,
+                                                                             float* db) {
   __shared__ float red[REDUCE_Y][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;

@@ -117,7 +117,8 @@ __device__ __forceinline__ void ldv(float (&d)[VEC], const float* p) {
 }
 
 // The kernels of an update are launched one ahead: each starts when the one before it has started everywhere, sets
-// itself up, and waits here until that one has completed before it touches what it works on.
+// itself up, and waits here until that one has completed before it touches what it works on. (What
+// that one writes is no const __restrict__ here therefore, whose loads may go by the non-coherent path and ahead of the wait.)
 __device__ __forceinline__ void release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(Grad p, Walk w, double* 
 // X = S_X u / (|u| + eps) as fp16 head and rest, from g and the m' that the norm pass left. Threads from 256 on
 // only join the sum.
 template <int VEC>
-__device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const double* __restrict__ parts, int n_parts, double eps,
+__device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const double* parts, int n_parts, double eps,
                                            __half* __restrict__ hi, __half* __restrict__ lo, int64_t ld_x) {
   double s = 0.0;
   for (int i = threadIdx.x; i < n_parts; i += blockDim.x) s += parts[i];
@@ -214,7 +215,7 @@ __device__ __forceinline__ void scale_pass(const Grad& p, const Walk& w, const d
 }
 
 template <int VEC>
-__global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* __restrict__ parts, int n_parts, double eps,
+__global__ void __launch_bounds__(256) muon_scale_kernel(Grad p, Walk w, const double* parts, int n_parts, double eps,
                                                          __half* __restrict__ hi, __half* __restrict__ lo, int64_t ld_x) {
   release_next();
   wait_for_last();
