@@ -74,10 +74,13 @@ __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 }
 
-// 1 / sqrt(v): the fast approximation (2 units in the last place) and one Newton step.
+// 1 / sqrt(v): the fast approximation (2 units in the last place) and one Newton step; not where that is 0 or infinite
+// (a variance that left fp32, or none and no eps), which the step would make NaN.
+// (1 / sqrtf(v) in its place: 98304 x 3584 in 248 us, against 227.)
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+  const float c = fmaf(-v * r, r, 1.0f);
+  return c == c ? fmaf(0.5f * r, c, r) : r;
 }
 
 // A thread's NV vectors of a row whose first element is the shift-th of its granule: vector t + k T holds the

@@ -212,8 +212,9 @@ mt_status mt_rmsnorm_bwd_noalloc(const mt_bf16* dy, const mt_bf16* x, const mt_b
  * mean, rstd (fp32 [rows] out, what the backward needs) may each be NULL. y may
  * be x (same row stride); they must not overlap otherwise. Pointers need the
  * alignment of their elements only; operands whose rows lie alike in their
- * 16-byte granules (same address and stride modulo 16 bytes) are faster. H above
- * 2^28: MT_ERR_UNSUPPORTED. */
+ * 16-byte granules (same address and stride modulo 16 bytes) are faster. Sums are
+ * fp32: a row whose squared deviations sum to more than that holds (elements of
+ * 1e19 and more) gets rstd = 0 and y = b. H above 2^28: MT_ERR_UNSUPPORTED. */
 mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, const mt_bf16* b, mt_bf16* y,
                            int64_t ld_y, float* mean, float* rstd, int64_t rows, int32_t H, float eps, void* stream);
 

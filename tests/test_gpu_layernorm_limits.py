@@ -1,0 +1,53 @@
+"""LayerNorm at the ends of fp32's range, and rows far from zero against their spread: the register kernels (rows of
+whole 16-byte granules, and of others) and the one that walks a row an element at a time give the same answers."""
+import numpy as np
+import pytest
+
+import helpers as H
+from host_offloaded_layer_b200 import _lib as L
+
+pytestmark = pytest.mark.gpu
+
+U, UB = 2.0 ** -24, 2.0 ** -8  # half a step of fp32 and of bf16, relative
+
+
+def _strided(rows, width, ld, fill=0.0):
+    import torch
+    return torch.full((rows, ld), fill, dtype=torch.bfloat16, device="cuda")
+
+
+def _forward(x, width, ld_y, g, b, eps):
+    """y, mean, rstd of rows x [rows, ld_x]."""
+    rows, ld_x = x.shape
+    y, mean, rstd = _strided(rows, width, ld_y), H.empty_f32(rows), H.empty_f32(rows)
+    L.mt_layernorm_fwd(x, ld_x, g, b, y, ld_y, mean, rstd, rows, width, eps)
+    return y[:, :width], mean, rstd
+
+
+# x's and y's row strides: whole granules alike, others alike, and unlike (the kernel for any operands)
+PATHS = [(0, 0), (1, 1), (8, 1)]
+
+
+@pytest.mark.parametrize("width", [8, 256, 1000, 3584, 5120, 8200])
+@pytest.mark.parametrize("pad_x,pad_y", PATHS)
+def test_variances_that_leave_fp32_and_none_at_all(width, pad_x, pad_y):
+    """Elements of +-1e20: their squares are infinite in fp32, rstd = 0 and y = b. A row without spread and eps = 0: rstd
+    is infinite and y NaN, as 0 times infinity is. In every kernel alike; the row between them is an ordinary one."""
+    import torch
+    gen = torch.Generator().manual_seed(width)
+    rows = 37
+    x = _strided(rows, width, width + pad_x)
+    x[:, :width] = torch.randn(rows, width, generator=gen).cuda()
+    big = torch.where(torch.arange(width) % 2 == 0, 1e20, -1e20).cuda()
+    x[3, :width] = big
+    x[5, :width] = 0.0
+    b = torch.randn(width, generator=gen).bfloat16().cuda()
+    y, mean, rstd = _forward(x, width, width + pad_y, None, b, 0.0)
+    torch.cuda.synchronize()
+    assert float(rstd[3]) == 0.0 and torch.equal(y[3], b)
+    assert float(rstd[5]) == float("inf") and bool(y[5].isnan().all()) and float(mean[5]) == 0.0
+    rest = [r for r in range(rows) if r not in (3, 5)]
+    assert bool(torch.isfinite(y[rest]).all()) and bool(torch.isfinite(rstd[rest]).all())
+    y, mean, rstd = _forward(x, width, width + pad_y, None, b, 1e-6)
+    torch.cuda.synchronize()
+    assert torch.equal(y[5], b) and abs(float(rstd[5]) - 1000.0) <= 4 * U * 1000 + 1e-3 * 1e-6
