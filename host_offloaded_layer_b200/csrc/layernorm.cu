@@ -83,6 +83,14 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return c == c ? fmaf(0.5f * r, c, r) : r;
 }
 
+// s / H: the product with the rounded 1 / H, and what it leaves of s divided likewise. Without that the mean of a row of
+// equal elements is a step beside them, which a small spread and eps make visible (H = 3584, elements of 1000, eps = 1e-6:
+// xh = 0.09 in place of 0). An infinite sum stays as it is. (s / H as one operation: 98304 x 3584 in 245 us, against 229.)
+__device__ __forceinline__ float row_mean(float s, float inv_h, float h) {
+  const float m = s * inv_h, left = fmaf(-m, h, s);
+  return left == left ? fmaf(left, inv_h, m) : m;
+}
+
 // A thread's NV vectors of a row whose first element is the shift-th of its granule: vector t + k T holds the
 // columns col[k] .. col[k] + 7, all in the row, or is absent. EDGE: rows may have elements outside their whole
 // granules; edge is the column of one that this lane has, or -1. (A mask for partial vectors instead, in the threads
@@ -155,7 +163,7 @@ struct LnFwd {
   int64_t ld_x, ld_y, rows, stride;  // stride: rows from one of a group's to its next; hop: elements, likewise
   int64_t hop_x, hop_y;
   int H, W;
-  float eps, inv_h;
+  float eps, inv_h, h;
 };
 
 // R rows at a time: one exchange of R sums serves them. Two, where registers allow; rows of 4097 to 5120 would leave
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_fwd_kernel(const __gr
     float q[R], mean[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mean[r] = s[r] * a.inv_h;
+      mean[r] = row_mean(s[r], a.inv_h, a.h);
       f2 sum = 0;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_wide_kernel(LnFwd a) {
     float s[1] = {0.f}, q[1] = {0.f};
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) s[0] += __bfloat162float(x[j]);
     group_sums<1>(s, blockDim.x >> 5, wig, 1, red[0]);
-    const float mean = s[0] * inv_h;
+    const float mean = row_mean(s[0], inv_h, static_cast<float>(a.H));
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
       const float c = __bfloat162float(x[j]) - mean;
       q[0] = fmaf(c, c, q[0]);
@@ -1011,6 +1019,7 @@ mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, con
   a.eps = eps;
   a.stride = 0;
   a.inv_h = 1.0f / static_cast<float>(H);
+  a.h = static_cast<float>(H);
   return layernorm_fwd_launch(a, as_stream(stream));
 }
 

@@ -51,3 +51,21 @@ def test_variances_that_leave_fp32_and_none_at_all(width, pad_x, pad_y):
     y, mean, rstd = _forward(x, width, width + pad_y, None, b, 1e-6)
     torch.cuda.synchronize()
     assert torch.equal(y[5], b) and abs(float(rstd[5]) - 1000.0) <= 4 * U * 1000 + 1e-3 * 1e-6
+
+
+@pytest.mark.parametrize("width", [3, 7, 56, 896, 897, 3584, 3592, 7168, 14336])
+@pytest.mark.parametrize("pad_x,pad_y", PATHS)
+def test_rows_of_equal_elements_have_their_element_as_mean(width, pad_x, pad_y):
+    """A bf16 element has 8 bits, and a sum of up to 2^16 equal ones fits fp32's 24 exactly, in whatever order: its quotient
+    by H is the element, so x - mean is 0, the variance 0 and y = b bit for bit."""
+    import torch
+    vals = torch.tensor([1000.0, 5.5, -0.3359375, 3.0, 1e-3, 250.0, -7e4, 255.0, 1.0078125]).bfloat16().cuda()
+    x = _strided(len(vals), width, width + pad_x)
+    x[:, :width] = vals[:, None]
+    gen = torch.Generator().manual_seed(width)
+    g, b = (torch.randn(width, generator=gen).bfloat16().cuda() for _ in range(2))
+    y, mean, rstd = _forward(x, width, width + pad_y, g, b, 1e-6)
+    torch.cuda.synchronize()
+    assert torch.equal(mean, vals.float())
+    assert torch.equal(y, b[None].expand_as(y))
+    assert bool(((rstd.double() - 1000.0).abs() <= 4 * U * 1000 + 1e-3).all())  # 1e-6 itself is half a step off in fp32
