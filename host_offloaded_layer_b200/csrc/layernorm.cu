@@ -409,6 +409,10 @@ __device__ __forceinline__ void leave_sums_anew(const LnBwd& a, float* sums, con
   leave_sums<NV, EDGE>(a, Cols<NV, EDGE>(tid - group * T, T, shift, a.H), sums, group, groups, dg, db, edge_dg, edge_db);
 }
 
+// Both backward kernels subtract the mean before they scale: x rstd - mean rstd, one instruction less, would be off by half a
+// step of mean rstd, which rows far from zero against their spread have in every xh and in dg (98304 x 3584: 366 us, against
+// 359; 32768 x 5120: 189 against 183).
+//
 // Rows with elements outside their whole granules: a row at a time, the next ones in flight.
 template <int NV, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __grid_constant__ LnBwd a) {
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
     if (to == ring_end) to = ring;
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     f2 s0 = 0, s1 = 0;
-    const f2 rs = f2_both(rstd), off = f2_both(-mean * rstd);
+    const f2 rs = f2_both(rstd), off = f2_both(-mean);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       uint32_t d[4], x[4];
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
       lds128(at + slice + k * T * 16, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f2 dv = f2_of(d[i]), xh = f2_fma(f2_of(x[i]), rs, off), w = f2_mul(dv, gain[k][i]);
+        const f2 dv = f2_of(d[i]), xh = f2_mul(f2_add(f2_of(x[i]), off), rs), w = f2_mul(dv, gain[k][i]);
         s0 = f2_add(s0, w);
         s1 = f2_fma(w, xh, s1);
         dg[k][i] = f2_fma(dv, xh, dg[k][i]);
@@ -506,15 +510,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
     }
     // absent vectors and the edge elements of other lanes hold dy = 0, which adds nothing to any sum
     float s[2] = {f2_sum(s0), f2_sum(s1)};
-    const float edge_w = edge_dy * edge_gain, edge_xh = fmaf(edge_x, rstd, -mean * rstd);
+    const float edge_w = edge_dy * edge_gain, edge_xh = (edge_x - mean) * rstd;
     s[0] += edge_w;
     s[1] = fmaf(edge_w, edge_xh, s[1]);
     edge_dg = fmaf(edge_dy, edge_xh, edge_dg);
     edge_db += edge_dy;
     group_sums<2>(s, W, wig, 1 + group, red[buf] + group * W * 2);
     buf ^= 1;
-    // dx = rstd w - rstd c1 - xh (rstd c2) + dres, from the ring again: registers that held w and xh meanwhile would spill
-    const f2 k1 = f2_both(-rstd * (s[0] * a.inv_h)), k2 = f2_both(-rstd * (s[1] * a.inv_h));
+    // dx = rstd w - rstd c1 - (x - mean) (rstd rstd c2) + dres, from the ring again: registers that held w and xh meanwhile would spill
+    const f2 k1 = f2_both(-rstd * (s[0] * a.inv_h)), k2 = f2_both(-rstd * (rstd * (s[1] * a.inv_h)));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       uint32_t o[4], r[4], d[4], x[4];
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_kernel(const __gr
       if (RES) lds128(at + 2 * slice + k * T * 16, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f2 v = f2_fma(f2_fma(f2_of(x[i]), rs, off), k2, k1);
+        f2 v = f2_fma(f2_add(f2_of(x[i]), off), k2, k1);
         v = f2_fma(f2_mul(f2_of(d[i]), gain[k][i]), rs, v);
         if (RES) v = f2_add(v, f2_of(r[i]));
         o[i] = f2_pack(v);
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       rs[r] = f2_both(next_rstd[r]);
-      off[r] = f2_both(-next_mean[r] * next_rstd[r]);
+      off[r] = f2_both(-next_mean[r]);
     }
     stats(row + R * a.stride);
     const uint32_t at = ring + slot * slot_bytes;
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
           lds128(at + r * slot_bytes + slice + k * T * 16, x);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f2 dv = f2_of(d[i]), xh = f2_fma(f2_of(x[i]), rs[r], off[r]), w = f2_mul(dv, gain[k][i]);
+            const f2 dv = f2_of(d[i]), xh = f2_mul(f2_add(f2_of(x[i]), off[r]), rs[r]), w = f2_mul(dv, gain[k][i]);
             s0 = f2_add(s0, w);
             s1 = f2_fma(w, xh, s1);
             dg[k][i] = f2_fma(dv, xh, dg[k][i]);
@@ -672,10 +676,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row + r * a.stride < a.rows) {
-        // dx = rstd w - rstd c1 - xh (rstd c2) + dres
+        // dx = rstd w - rstd c1 - (x - mean) (rstd rstd c2) + dres
         float rstd, same;
         f2_split(rs[r], rstd, same);
-        const f2 k1 = f2_both(-rstd * (s[2 * r] * a.inv_h)), k2 = f2_both(-rstd * (s[2 * r + 1] * a.inv_h));
+        const f2 k1 = f2_both(-rstd * (s[2 * r] * a.inv_h)), k2 = f2_both(-rstd * (rstd * (s[2 * r + 1] * a.inv_h)));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           uint32_t o[4], q[4], d[4], x[4];
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) layernorm_bwd_bulk_kernel(const
           if (RES) lds128(at + r * slot_bytes + 2 * slice + k * T * 16, q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            f2 v = f2_fma(f2_fma(f2_of(x[i]), rs[r], off[r]), k2, k1);
+            f2 v = f2_fma(f2_add(f2_of(x[i]), off[r]), k2, k1);
             v = f2_fma(f2_mul(f2_of(d[i]), gain[k][i]), rs[r], v);
             if (RES) v = f2_add(v, f2_of(q[i]));
             o[i] = f2_pack(v);

@@ -69,3 +69,33 @@ def test_rows_of_equal_elements_have_their_element_as_mean(width, pad_x, pad_y):
     assert torch.equal(mean, vals.float())
     assert torch.equal(y, b[None].expand_as(y))
     assert bool(((rstd.double() - 1000.0).abs() <= 4 * U * 1000 + 1e-3).all())  # 1e-6 itself is half a step off in fp32
+
+
+@pytest.mark.parametrize("rows,width", [(40, 256), (300, 1160), (64, 3584), (300, 1153), (20, 5120), (16, 5113), (7, 8200)])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_backward_of_rows_far_from_zero(rows, width, pad):
+    """Rows at 1000, one bf16 step (4) up or down here and there, with a mean of 1000.1 and rstd 50: xh is the difference
+    rounded (U) and the product rounded (U), whatever the mean's size. dx = rstd (w - c1) - (x - mean) rstd (rstd c2)
+    + dres as written; sums of n terms carry 64 U of their absolute sum (test_gpu_norm_rope), the column sums the chain
+    that is written there."""
+    import torch
+    gen = torch.Generator().manual_seed(width + pad)
+    ld = width + pad
+    x, dy, dx = _strided(rows, width, ld), _strided(rows, width, ld), _strided(rows, width, ld)
+    x[:, :width] = (1000 + 4 * torch.randint(-1, 2, (rows, width), generator=gen)).cuda()
+    dy[:, :width] = torch.randn(rows, width, generator=gen).cuda()
+    mean, rstd = torch.full((rows,), 1000.1, device="cuda"), torch.full((rows,), 50.0, device="cuda")
+    dg, db = H.empty_f32(width), H.empty_f32(width)
+    n = L.mt_layernorm_bwd_workspace_bytes(rows, width)
+    L.mt_layernorm_bwd(dy, ld, x, ld, None, mean, rstd, None, 0, dx, ld, dg, db, rows, width, H.workspace(n), n)
+    torch.cuda.synchronize()
+    w, x64 = H.host_f64(dy[:, :width].contiguous()), H.host_f64(x[:, :width].contiguous())
+    m, r = H.host_f64(mean)[:, None], H.host_f64(rstd)[:, None]
+    xh = (x64 - m) * r
+    c1, c2 = w.mean(1, keepdims=True), (w * xh).mean(1, keepdims=True)
+    ref = r * (w - c1 - xh * c2)
+    e1, e2 = 66 * U * np.abs(w).mean(1, keepdims=True), 70 * U * np.abs(w * xh).mean(1, keepdims=True)
+    err = r * (4 * U * (np.abs(w) + np.abs(c1) + np.abs(xh * c2)) + e1 + np.abs(xh) * e2 + 3 * U * np.abs(xh * c2))
+    assert np.all(np.abs(H.host_f64(dx[:, :width].contiguous()) - ref) <= (UB + 2 * U) * np.abs(ref) + 1.01 * err)
+    chain = rows / 32 + 64 + 4 * 148 / 8
+    assert np.all(np.abs(H.host_f64(dg) - (w * xh).sum(0)) <= (chain + 3) * U * np.abs(w * xh).sum(0))
