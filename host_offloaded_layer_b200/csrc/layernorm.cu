@@ -36,6 +36,7 @@ using namespace vec;
 constexpr int SMS = 148;            // the partial rows of dg and db are counted for a whole B200, so that sums do not depend on the device
 constexpr int DEPTH = 3;            // stages of a ring: two in flight, one being read
 constexpr int MAX_H_REG = 8192;     // the widest row that 16 warps of two vectors a thread hold
+constexpr int MAX_H = 1 << 28;      // and the widest of all, so that columns and their doubles count in 32 bits
 
 __device__ __forceinline__ void group_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -1003,7 +1004,7 @@ mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, con
   if (rows < 0 || H <= 0 || !(eps >= 0.f)) return fail(MT_ERR_INVALID_ARG, "layernorm_fwd: need rows >= 0, H > 0, eps >= 0");
   if (ld_x < H || ld_y < H) return fail(MT_ERR_INVALID_ARG, "layernorm_fwd: row stride smaller than H");
   if (x && y == x && ld_y != ld_x) return fail(MT_ERR_INVALID_ARG, "layernorm_fwd: in place needs ld_x == ld_y");
-  if (H > (1 << 28)) return fail(MT_ERR_UNSUPPORTED, "layernorm_fwd: H above 2^28");
+  if (H > MAX_H) return fail(MT_ERR_UNSUPPORTED, "layernorm_fwd: H above 2^28");
   if (!aligned_to(x, 2) || !aligned_to(y, 2) || !aligned_to(g, 2) || !aligned_to(b, 2) || !aligned_to(mean, 4) ||
       !aligned_to(rstd, 4))
     return fail(MT_ERR_ALIGNMENT, "layernorm_fwd: pointers must be aligned to their elements");
@@ -1028,7 +1029,7 @@ mt_status mt_layernorm_fwd(const mt_bf16* x, int64_t ld_x, const mt_bf16* g, con
 }
 
 uint64_t mt_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H) {
-  if (rows < 0 || H <= 0) return 0;
+  if (rows < 0 || H <= 0 || H > MAX_H) return 0;
   return bwd_ws_bytes(rows, H);
 }
 
@@ -1040,7 +1041,7 @@ mt_status mt_layernorm_bwd(const mt_bf16* dy, int64_t ld_dy, const mt_bf16* x, i
   if (rows < 0 || H <= 0) return fail(MT_ERR_INVALID_ARG, "layernorm_bwd: need rows >= 0, H > 0");
   if (ld_dy < H || ld_x < H || ld_dx < H || (dres && ld_dres < H))
     return fail(MT_ERR_INVALID_ARG, "layernorm_bwd: row stride smaller than H");
-  if (H > (1 << 28)) return fail(MT_ERR_UNSUPPORTED, "layernorm_bwd: H above 2^28");
+  if (H > MAX_H) return fail(MT_ERR_UNSUPPORTED, "layernorm_bwd: H above 2^28");
   if (rows != 0 && ((dx == dy && ld_dx != ld_dy) || (dres && dx == dres && ld_dx != ld_dres) || dx == x))
     return fail(MT_ERR_INVALID_ARG, "layernorm_bwd: dx may only be dy or dres itself, with the same row stride");
   if (!aligned_to(dy, 2) || !aligned_to(x, 2) || !aligned_to(g, 2) || !aligned_to(dres, 2) || !aligned_to(dx, 2) ||

@@ -62,3 +62,12 @@ def test_mrope_refuses(bad, name):
     a = dict(x=P, ld_x=32, y=P + 1024, ld_y=32, pos=P, ld_pos=4, sections=[4, 4], rows=4, heads=2, d=16, theta=1e4)
     a.update(bad)
     _refused(name, L.mt_mrope, *a.values())
+
+
+def test_layernorm_backward_workspace_is_nothing_for_a_width_that_the_call_refuses():
+    for rows in (0, 1, 98304):
+        assert L.mt_layernorm_bwd_workspace_bytes(rows, 1 << 28) >= 2 * (1 << 28) * 4
+        assert L.mt_layernorm_bwd_workspace_bytes(rows, (1 << 28) + 1) == 0
+        assert L.mt_layernorm_bwd_workspace_bytes(rows, 2 ** 31 - 1) == 0
+    _refused("MT_ERR_UNSUPPORTED", L.mt_layernorm_bwd, P, 1 << 29, P + 256, 1 << 29, P, P, P, None, 0, P + 1024, 1 << 29, P, P, 2,
+             (1 << 28) + 1, P, 1 << 62)
