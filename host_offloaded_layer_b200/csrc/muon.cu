@@ -43,6 +43,9 @@ constexpr double NS64_A = 3.4445, NS64_B = -4.7750, NS64_C = 2.0315;
 constexpr float S_X = 16384.f, S_A = 16384.f, S_P = 8192.f;
 constexpr int64_t MAX_ELEMENTS = 1ll << 36;  // no device holds more; sizes and tile numbers stay in range
 constexpr int TINY = 64;  // the widest short side of the Gram path
+// Paths, splits of K and workspaces are chosen for a whole B200's SMs whatever the device: a workspace's size and a
+// result's order of sums depend on the matrix alone.
+constexpr int SMS = 148;
 
 // ------------------------------------------------------------------ momentum, norm, head and rest of X
 struct Grad {
@@ -1211,12 +1214,11 @@ mt_status ns_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensor
 
 // 0: 256 x 256 tiles on SM pairs; else 128 x 128 tiles with K split over that many CTAs.
 int pick_split(const NsArgs& e) {
-  const int sms = num_sms();
-  if (ns_tiles(e, 256) * 2 >= sms / 2) return 0;
+  if (ns_tiles(e, 256) * 2 >= SMS / 2) return 0;
   const int tiles = ns_tiles(e, 128), atoms = (e.K + 63) / 64;
   int split = 1;
   // a split costs the meeting of the shares, about 2 us: taken while each CTA keeps 16 atoms (2 us)
-  while (split < 8 && tiles * split * 2 <= sms && atoms >= split * 32) split *= 2;
+  while (split < 8 && tiles * split * 2 <= SMS && atoms >= split * 32) split *= 2;
   return split;
 }
 
@@ -1567,9 +1569,7 @@ struct Plan {
 };
 
 // Whether all steps run as one kernel: each product's tiles fit a B200 about once, so that whole SM pairs on
-// 256 x 256 tiles would not be faster. (Counted for 148 SMs whatever the device, like the split: a workspace's size
-// and a result's order of sums depend on the matrix alone.)
-constexpr int SMS = 148;
+// 256 x 256 tiles would not be faster.
 bool pick_fused(int64_t m, int64_t n) {
   const int64_t tm = (m + 127) / 128, tn = (n + 127) / 128;
   return tm * tn <= SMS && tm * (tm + 1) / 2 <= SMS;
@@ -1592,7 +1592,7 @@ Plan plan(int64_t rows, int64_t cols, void* ws) {
   p.n = std::max(rows, cols);
   Bump b(ws, ~0ull);
   if (p.m <= TINY) {
-    p.parts = static_cast<int>(std::min<int64_t>(148, (p.n + CHUNK - 1) / CHUNK));
+    p.parts = static_cast<int>(std::min<int64_t>(SMS, (p.n + CHUNK - 1) / CHUNK));
     p.gram = b.take<double>(static_cast<int64_t>(p.parts) * p.m * p.m);
   } else {
     p.parts = NORM_PARTS;

@@ -45,3 +45,15 @@ def test_workspace_holds_three_copies_of_x_and_its_square_matrices():
         assert need <= n <= need + 2 * m * up(m) + 148 * 128 * 128 * 4 + 9 * 256
     for rows, cols in ((1, 1), (64, 100000), (100000, 3)):
         assert 0 < L.mt_muon_workspace_bytes(rows, cols) <= 148 * 64 * 64 * 8 + 64 * 64 * 4 + 512
+
+
+def test_the_order_of_sums_is_chosen_by_the_matrix_alone():
+    """No function that chooses a path, a split of K or the parts of a workspace asks for the device's SMs (read from the
+    source: there is one kind of device to run on)."""
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "host_offloaded_layer_b200", "csrc", "muon.cu")
+    with open(path) as f:
+        code = f.read()
+    for name in ("int pick_split(", "bool pick_fused(", "int fused_split(", "bool pair_first_steps(", "Plan plan("):
+        at = code.index("\n" + name)
+        assert "num_sms" not in code[at:code.index("\n}", at)], name
