@@ -17,8 +17,10 @@
 // from a two-term X (fp16 head + fp16 rest, 22 bits), while the products take the head alone: a rounding of
 // b A + c A^2 moves strong directions only, where nothing is amplified. In the last two steps, which amplify
 // little, the polynomial takes a on its diagonal and X its head only. Against the same steps in fp64 the
-// result is 1e-3 (2-norm) off before its rounding to bf16, which alone is 1.7e-3, for Gaussian matrices and
-// for a few strong directions over noise alike (64..4096 wide); fp16 throughout is up to 1.4e-2 off.
+// result is 1e-3 to 1.5e-3 (root of the squares' sum) off before its rounding to bf16, which alone is 1.7e-3, for
+// Gaussian matrices, and up to 3e-3 for one or a few strong directions with or without noise (emulated for short sides
+// of 65..1500); fp16 throughout is up to 1.4e-2 off. Where one direction has elements of equal size, all roundings of
+// an operand fall the same way: 4e-3 at most of those tried.
 // |u|_F is summed in fp64, so that no magnitude of g that fp32 holds over- or underflows.
 //
 // Matrices whose short side is at most 64 take no tensor cores: their Gram matrix (in fp64) is all that the
@@ -1757,7 +1759,9 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
     // A' = (a I + P) A (a I + P) = a^2 A + 2 a M + P M, M = P A, and X'' = (a I + P') (a I + P) X =
     // a^2 X + Q X, Q = a (P + P') + P' P. All of them commute, so each of the five products takes half its tiles:
     // 3 m^2 n + 5 m^3 multiply-adds where two steps take 6 m^2 n + 2 m^3. As accurate as two steps (the noise of
-    // A's rounding has one step to grow); three steps on one Gram matrix lose a factor of three.
+    // A's rounding has one step to grow), but for one direction with elements of equal size: a^2 + Q = 1.1 there, with Q
+    // = -10.8 and X's head rounded the same way all over, where two steps have a + P = 0.7 with P = -2.7 (1200 x 2600 of
+    // equal elements: 1.8e-2 off, 1200 x 1300: 1.2e-3). Three steps on one Gram matrix lose a factor of three.
     constexpr float S_Q = 4096.f;  // |Q| <= a^2 = 11.9
     MT_TRY(operand_maps(&sq_c, Operand{p.C, p.ld_a, false, p.m}, m));
     MT_TRY(ns_product(x_short[0], x_short[0], gram_args(m, n, p.A, p.ld_a), st));

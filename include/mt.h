@@ -533,12 +533,21 @@ uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols);
  * m_in, m_out: fp32 momentum, rows ld_m elements apart; m_out may be m_in (the
  * buffer is then updated in place); both NULL: u = g. o: bf16, rows ld_o
  * elements apart, the direction to take off the weights. A matrix taller than
- * wide uses A = X^T X. The products run on the tensor cores in fp16 with fp32
- * sums (short sides of at most 64: fp32 up to 5 steps, fp64 beyond); before its
- * rounding to bf16 the result is within about 2e-3 (2-norm) of the same steps in
- * fp64 for 5 steps. Elements
- * between cols and a row's stride are neither read nor written. A g or m that
- * holds infinities or NaN gives NaN. Deterministic: fixed order of every sum.
+ * wide uses A = X^T X. Elements between cols and a row's stride are neither read
+ * nor written. A g or m that holds infinities or NaN gives a result of NaN.
+ * Deterministic: fixed order of every sum.
+ * Accuracy: the products run on the tensor cores in fp16 with fp32 sums (short
+ * sides of at most 64: fp32 up to 5 steps, fp64 beyond). Against the same steps in
+ * fp64, relative in the root of the sum of squares, before the rounding to bf16:
+ *   5 steps: 1e-3 to 3e-3. A matrix of one direction whose elements have one or a few
+ *     sizes, so that their roundings fall the same way: up to 5e-3, and 2e-2 where its
+ *     first two steps share a Gram matrix (more than 148 tiles of 128 x 128, the
+ *     long side at least twice the short one). Short sides of at most 64: below 1e-3.
+ *   More steps: up to twice that at 7, 1e-2 at 20, in directions of at least 2^-14 of
+ *     |u|. Much weaker ones drown in the noise of X's 22 bits, which grows by 3.44 a step
+ *     as they do (short sides of at most 64: they do not, but below 2^-21 of |u| they end
+ *     in proportion to their size, however many the steps).
+ *   The result is bounded for any number of steps: no singular value above 1.23 |scale|.
  * g, m_in, m_out, o: aligned to their elements (16-byte aligned rows of 4
  * elements, 8 for o, are faster), none overlapping another but m_in = m_out.
  * ws: device, 256-byte aligned, not shared with a call that may run at the same

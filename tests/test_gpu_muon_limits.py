@@ -142,3 +142,87 @@ def test_short_sides_stay_bounded_for_any_number_of_steps(rows, cols, kind, step
     o = _update(_matrix(kind, rows, cols, steps).cuda(), L.make_muon_cfg(steps=steps))
     assert bool(torch.isfinite(o).all()) and float(torch.linalg.matrix_norm(o, 2)) <= 1.2024 * (1 + UB)
     assert float(torch.linalg.matrix_norm(o, 2)) > 0.5  # nor does the strongest direction vanish
+
+
+# ---------------------------------------------------------------- tensor cores: short sides above 64
+def _fp16_bound(s, steps, pair):
+    """What half a step (2^-11) in every fp16 operand does to the results of singular values s, relative to them, to first
+    order and with all the roundings of a matrix falling the same way: the sum over the operands' derivatives. That is
+    what a matrix of equal entries can come to; roundings that fall either way stay far below. (X's rest in the first
+    steps leaves 2^-22, which is nothing beside; a factor of 1.1 covers the second order.)"""
+    import torch
+    n_roundings = 6 * steps + 2
+    e = torch.zeros(n_roundings, len(s), dtype=torch.float64, requires_grad=True)
+    it = iter(range(n_roundings))
+    r = lambda v: v * (1 + e[next(it)])  # noqa: E731  one operand, rounded
+    x, done = s.clone(), 0
+    if pair and steps >= 4:
+        h = r(x)
+        a = r(h * h)
+        p = r(NB * a + NC * a * a)
+        m = r(p * a)
+        a1 = r(NA ** 2 * a + 2 * NA * m + p * m)
+        p1 = r(NB * a1 + NC * a1 * a1)
+        x, done = NA ** 2 * x + r(NA * (p + p1) + p1 * p) * h, 2
+    for i in range(done, steps):
+        h = r(x)
+        a = r(h * h)
+        if i < steps - 2:
+            x = NA * x + r(NB * a + NC * a * a) * h
+        else:  # a I in the same operand: its diagonal rounds too
+            x = (r(NB * a + NC * a * a) + r(torch.full_like(a, NA))) * h
+    g, = torch.autograd.grad(x.sum(), e)
+    return 1.1 * 2.0 ** -11 * g.abs().sum(0) / x.detach().abs()
+
+
+@pytest.mark.parametrize("steps", [1, 2, 5, 7])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(65, 200), (300, 128), (333, 500), (1200, 1300), (1200, 2600), (2600, 1200), (100, 19000)])
+def test_other_matrices_follow_the_exact_steps(rows, cols, kind, steps):
+    """Against float64 steps, whatever the matrix lacks: the roundings' bound of its singular values (those above 1e-6: in
+    the others nothing but the noise of X's two terms, 2^-22 of |u| in the 2-norm each step, grown by 3.4445 a step),
+    and bf16's."""
+    import torch
+    g = _matrix(kind, rows, cols, rows + steps).cuda()
+    cfg = L.make_muon_cfg(steps=steps)
+    ref = _exact(g.double(), steps, cfg.eps)
+    off = (_update(g, cfg) - ref).norm()
+    u = g.double()
+    s = torch.linalg.svdvals(u / (u.norm() + cfg.eps)).cpu()
+    s = s[s > 1e-6]
+    short, long = min(rows, cols), max(rows, cols)
+    shared = long >= 2 * short and -(-short // 128) * -(-long // 128) > 148  # the first two steps on one Gram matrix
+    rel = float(_fp16_bound(s, steps, shared).max())
+    noise = sum(2.0 ** -22 * NA ** k for k in range(1, steps + 1))
+    allowed = (1.01 * UB + rel) * ref.norm() + noise
+    assert off <= allowed
+    if steps == 5:  # and what the header states, with bf16's own share of 2^-8 / sqrt(3) at most
+        stated = 3e-3 if kind in ("full", "rows four times", "strong + 1e-3", "rank 8") else 2e-2 if shared else 5e-3
+        assert off <= (stated + 2.3e-3) * ref.norm()
+
+
+@pytest.mark.parametrize("steps", [20, 100])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(65, 200), (300, 128), (1200, 2600)])
+def test_other_matrices_stay_bounded_for_any_number_of_steps(rows, cols, kind, steps):
+    """The polynomial maps [0, 1.2024] into itself, and up to 1.264 back below: 2e-2 of roundings do not lead out."""
+    import torch
+    o = _update(_matrix(kind, rows, cols, steps).cuda(), L.make_muon_cfg(steps=steps))
+    assert bool(torch.isfinite(o).all())
+    top = float(torch.linalg.matrix_norm(o.float(), 2))
+    assert 0.5 < top <= 1.23
+
+
+@pytest.mark.parametrize("where", ["g", "m"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("rows,cols,steps", [(30, 500, 5), (500, 30, 5), (30, 500, 8), (1, 64, 5), (250, 500, 5), (500, 250, 1),
+                                             (1200, 1300, 5), (2600, 1200, 5)])
+def test_one_infinity_or_nan_makes_the_whole_result_nan(rows, cols, steps, bad, where):
+    import torch
+    gen = torch_generator(rows)
+    g, m = (torch.randn(rows, cols, generator=gen).cuda() for _ in range(2))
+    (g if where == "g" else m)[rows // 2, cols // 3] = bad
+    m_out = torch.empty_like(m)
+    o = _update(g, L.make_muon_cfg(steps=steps), m, m_out)
+    assert bool(o.isnan().all())
+    assert int((~torch.isfinite(m_out)).sum()) == 1  # the momentum is element by element
