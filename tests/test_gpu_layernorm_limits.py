@@ -99,3 +99,45 @@ def test_backward_of_rows_far_from_zero(rows, width, pad):
     assert np.all(np.abs(H.host_f64(dx[:, :width].contiguous()) - ref) <= (UB + 2 * U) * np.abs(ref) + 1.01 * err)
     chain = rows / 32 + 64 + 4 * 148 / 8
     assert np.all(np.abs(H.host_f64(dg) - (w * xh).sum(0)) <= (chain + 3) * U * np.abs(w * xh).sum(0))
+
+
+@pytest.mark.parametrize("lds,offs", [((0, 1, 2, 3), (0, 0, 0, 0)), ((8, 8, 8, 8), (0, 0, 0, 4)), ((8, 0, 8, 16), (0, 1, 0, 0)),
+                                      ((0, 0, 0, 0), (0, 0, 0, 0))])
+@pytest.mark.parametrize("rows,width", [(700, 512), (20000, 72), (130, 9000)])
+def test_backward_of_operands_that_lie_unlike_and_of_one_sum_alone(rows, width, lds, offs):
+    """dy, x, dres and dx with row strides and offsets of their own, in the kernels for any operands where these differ;
+    dg and db each without the other are the same bit for bit. Bounds as in test_backward_of_rows_far_from_zero."""
+    import torch
+    gen = torch.Generator().manual_seed(width)
+    views = []
+    for extra, off in zip(lds, offs):
+        ld = width + extra
+        store = torch.full((off + rows * ld + 8,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        views.append((torch.as_strided(store, (rows, width), (ld, 1), off), ld))
+        views[-1][0].copy_(torch.randn(rows, width, generator=gen).cuda())
+    (dy, ld_dy), (x, ld_x), (dres, ld_dres), (dx, ld_dx) = views
+    g = torch.randn(width, generator=gen).bfloat16().cuda()
+    mean, rstd = torch.randn(rows, generator=gen).cuda(), (0.5 + torch.rand(rows, generator=gen)).cuda()
+    n = L.mt_layernorm_bwd_workspace_bytes(rows, width)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    outs = [(H.empty_f32(width), H.empty_f32(width)), (H.empty_f32(width), None), (None, H.empty_f32(width))]
+    got = []
+    for dg, db in outs:
+        dx.fill_(float("nan"))
+        L.mt_layernorm_bwd(dy, ld_dy, x, ld_x, g, mean, rstd, dres, ld_dres, dx, ld_dx, dg, db, rows, width, ws, n)
+        torch.cuda.synchronize()
+        got.append(dx.clone())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[2][1])
+    dy64, x64, r64, g64 = (H.host_f64(t.contiguous()) for t in (dy, x, dres, g))
+    m, r = H.host_f64(mean)[:, None], H.host_f64(rstd)[:, None]
+    xh, w = (x64 - m) * r, dy64 * g64
+    c1, c2 = w.mean(1, keepdims=True), (w * xh).mean(1, keepdims=True)
+    ref = r * (w - c1 - xh * c2) + r64
+    e1, e2 = 70 * U * np.abs(w).mean(1, keepdims=True), 74 * U * np.abs(w * xh).mean(1, keepdims=True)
+    err = r * (5 * U * (np.abs(w) + np.abs(c1) + np.abs(xh * c2)) + e1 + np.abs(xh) * e2 + 3 * U * np.abs(xh * c2))
+    assert np.all(np.abs(H.host_f64(got[0]) - ref) <= (UB + 2 * U) * np.abs(ref) + 1.01 * err)
+    chain = rows / 32 + 64 + 4 * 148 / 8
+    assert np.all(np.abs(H.host_f64(outs[0][0]) - (dy64 * xh).sum(0)) <= (chain + 3) * U * np.abs(dy64 * xh).sum(0))
+    assert np.all(np.abs(H.host_f64(outs[0][1]) - dy64.sum(0)) <= chain * U * np.abs(dy64).sum(0))
+    assert L.mt_device_error(clear=True) == 0
