@@ -1240,7 +1240,7 @@ struct TinyArgs {
   int tall;    // rows are the long side
   int steps;
   float scale;
-  double eps, floor;  // floor: added to the diagonal of X X^T in fp64
+  double eps, floor;  // floor: added to the diagonal of X X^T in fp64, relative to its trace
   double* gram;   // [parts][m * m]; the first becomes their sum, and then r
   int parts;
   __nv_bfloat16* o;
@@ -1438,9 +1438,9 @@ constexpr int TINY_SMEM = (6 * TINY * TINY + 4 * TINY_ROWS * TINY) * sizeof(T);
 // A is never formed anew from X: what rounding leaves in directions that u lacks, of either sign, grows by a^2 = 11.9 a
 // step, and the polynomial of a negative eigenvalue that has grown to about one only grows. In fp32 five steps stay
 // within 7e-4 of exact ones (48 equal rows; 2e-4 for rank one over noise of 1e-3), six within 3e-3, eight are off by
-// the result itself. More than five are therefore taken in fp64, and A starts with `floor` added to its diagonal, more
-// than what the roundings of the Gram sums and of a step can take off (a sum's chain of additions, and 512, times 2^-53:
-// the rows' absolute products have a 2-norm of at most |X|_F^2 = 1). No eigenvalue turns negative then, for any number of
+// the result itself. More than five are therefore taken in fp64, and A starts with `floor` of its trace added to its
+// diagonal, more than what the roundings of the Gram sums and of a step can take off (a sum's chain of additions, and 512,
+// times 2^-53: the rows' absolute products have a 2-norm of at most the trace). No eigenvalue turns negative then, for any number of
 // steps: the result is q(A) u, the exact steps but in directions weaker than sqrt(floor), some 2^-22 of |u|, which
 // come out weaker than exact steps have them after a dozen. 60 x 20000, ten steps: 127 us, 84 in fp32.
 template <class T>
@@ -1469,7 +1469,7 @@ __global__ void __cluster_dims__(TINY_CTAS, 1, 1) __launch_bounds__(256) muon_ti
   for (int q = 0; q < TINY * TINY / 256; ++q) {
     const int e = threadIdx.x + q * 256;
     const bool diag = e / TINY == e % TINY;
-    A[e / TINY][e % TINY] = static_cast<T>(own[q] * inv * inv + (sizeof(T) == 8 && diag ? a.floor : 0.0));
+    A[e / TINY][e % TINY] = static_cast<T>((own[q] + (sizeof(T) == 8 && diag ? a.floor * sum : 0.0)) * inv * inv);
     Q[e / TINY][e % TINY] = diag ? T(1) : T(0);
   }
   cluster_sync();  // every CTA has started, and holds A

@@ -133,6 +133,25 @@ def test_short_sides_follow_the_exact_steps(rows, cols, kind, steps):
     assert off <= allowed, (float(off / ref.norm()), float(allowed / ref.norm()))
 
 
+@pytest.mark.parametrize("steps", [5, 6, 12, 20])
+@pytest.mark.parametrize("ratio", [1e-3, 1e-6, 1e-9])
+@pytest.mark.parametrize("rows,cols", [(48, 2000), (500, 30)])
+def test_short_sides_under_an_eps_that_dwarfs_the_norm(rows, cols, ratio, steps):
+    """X starts at |u| / eps, as small as it may be, and the steps raise it. Gaussian rows have singular values within a
+    factor of two of one another: what is passed on of a relative 2^-40 is as in the test above, and five steps in fp32
+    stay within the header's 1e-3."""
+    import torch
+    g = torch.randn(rows, cols, generator=torch_generator(steps))
+    g = (g * (ratio / float(g.norm()))).cuda()
+    cfg = L.make_muon_cfg(steps=steps, eps=1.0)
+    ref = _exact(g.double(), steps, cfg.eps)
+    s = torch.linalg.svdvals(g.double().cpu() / (g.double().cpu().norm() + cfg.eps))
+    x, pass_on = _after(s, steps)
+    floor = 1400 * 2.0 ** -53 * (ratio * ratio)  # 512, and a chain of less than 800, of the trace
+    allowed = 1.01 * UB * ref.norm() + (1e-3 * ref.norm() if steps <= 5 else (x * pass_on * (floor / (2 * s * s) + 2.0 ** -40)).norm())
+    assert (_update(g, cfg) - ref).norm() <= allowed
+
+
 @pytest.mark.parametrize("steps", [30, 100])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("rows,cols", [(48, 2000), (300, 64)])
