@@ -5,7 +5,7 @@
 //
 // with (a, b, c) = (3.4445, -4.7750, 2.0315), X on its short side (A = X^T X and X <- a X + X (b A + c A^2)
 // where the matrix is taller than wide: the tensor cores read either operand in either order, so nothing is
-// transposed). Written m <= n for the two sides, a step is m^2 n + m^3 + 2 m^2 n multiply-adds when the two
+// transposed). Written m <= n for the two sides, a step is m^2 n + m^3 + 2 m^2 n operations when the two
 // symmetric products compute only the tiles on and below the diagonal and store each twice.
 //
 // Number formats. The operands of the products are fp16, the sums fp32. bf16 operands, 8 bits, leave the
@@ -1585,7 +1585,7 @@ int fused_split(int64_t m, int64_t n) {
   return atoms - atoms / std::max<int64_t>(1, split) >= 16 ? static_cast<int>(split) : 1;
 }
 
-// Whether the first two steps of a matrix this wide share a Gram matrix: 3 m^2 n of products saved for 3 m^3 more.
+// Whether the first two steps of a matrix this wide share a Gram matrix: 3 m^2 n operations saved for 3 m^3 more.
 bool pair_first_steps(int64_t m, int64_t n) { return n >= 2 * m; }
 
 Plan plan(int64_t rows, int64_t cols, void* ws) {
@@ -1758,7 +1758,7 @@ mt_status muon_general(const Grad& g, const mt_muon_cfg& c, mt_bf16* o, int64_t 
     // The first two steps on one Gram matrix: with P = b A + c A^2 the second step's is
     // A' = (a I + P) A (a I + P) = a^2 A + 2 a M + P M, M = P A, and X'' = (a I + P') (a I + P) X =
     // a^2 X + Q X, Q = a (P + P') + P' P. All of them commute, so each of the five products takes half its tiles:
-    // 3 m^2 n + 5 m^3 multiply-adds where two steps take 6 m^2 n + 2 m^3. As accurate as two steps (the noise of
+    // 3 m^2 n + 5 m^3 operations where two steps take 6 m^2 n + 2 m^3. As accurate as two steps (the noise of
     // A's rounding has one step to grow), but for one direction with elements of equal size: a^2 + Q = 1.1 there, with Q
     // = -10.8 and X's head rounded the same way all over, where two steps have a + P = 0.7 with P = -2.7 (1200 x 2600 of
     // equal elements: 1.8e-2 off, 1200 x 1300: 1.2e-3). Three steps on one Gram matrix lose a factor of three.

@@ -228,7 +228,8 @@ uint64_t mt_layernorm_bwd_workspace_bytes(int64_t rows, int32_t H);
  * overwritten; each may be NULL; zeros for rows = 0). mean, rstd: of the
  * forward. g may be NULL (a gain of 1). Rows as in mt_layernorm_fwd, each with
  * a stride of its own. dx may be dy or dres (same row stride). ws: device, 16-byte
- * aligned, not shared with a call that may run at the same time. */
+ * aligned, not shared with a call that may run at the same time; demanded without dg
+ * and db too. */
 mt_status mt_layernorm_bwd(const mt_bf16* dy, int64_t ld_dy, const mt_bf16* x, int64_t ld_x, const mt_bf16* g,
                            const float* mean, const float* rstd, const mt_bf16* dres, int64_t ld_dres, mt_bf16* dx,
                            int64_t ld_dx, float* dg, float* db, int64_t rows, int32_t H, void* ws, uint64_t ws_bytes,
@@ -548,6 +549,8 @@ uint64_t mt_muon_workspace_bytes(int64_t rows, int64_t cols);
  *     as they do (short sides of at most 64: they do not, but below 2^-21 of |u| they end
  *     in proportion to their size, however many the steps).
  *   The result is bounded for any number of steps: no singular value above 1.23 |scale|.
+ *   An eps above 1e6 |u| costs bits (X's elements are held to 2^-38), but not where the
+ *     short side is at most 64.
  * g, m_in, m_out, o: aligned to their elements (16-byte aligned rows of 4
  * elements, 8 for o, are faster), none overlapping another but m_in = m_out.
  * ws: device, 256-byte aligned, not shared with a call that may run at the same
